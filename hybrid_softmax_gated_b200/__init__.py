@@ -16,6 +16,11 @@ The layer ("Attend Locally, Remember Linearly", technical summary §2.1 and
 and the softmax teacher layer it replaces (TeacherLayer, technical summary
 §1 "KV Cache Growth"): frame N attends to the clean keys/values of frames
 0..N-1, kept in a KV cache, and bidirectionally to its own.
+
+For softmax layers whose sequences differ in length there is a paged cache
+(PagedCache, PagedBatch): new keys and values are written into pages, as they
+are or quantised to 8 bits, and attended to with an optional rolling window
+and sinks.  RotaryAxes gives q and k rotary positions with up to four axes.
 """
 from __future__ import annotations
 
@@ -33,6 +38,9 @@ ARL2_BF16, ARL2_FP32 = 0, 1
 ARL2_IMPL_AUTO, ARL2_IMPL_SIMT = 0, 1
 ARL2_GATE_HEADWISE, ARL2_GATE_ELEMENTWISE = 0, 1
 ARL2_ACCESS_FRAME, ARL2_ACCESS_TOKEN = 0, 1
+ARL2_PAIRS_ADJACENT, ARL2_PAIRS_HALVES = 0, 1
+ARL2_FREQS_PER_AXIS, ARL2_FREQS_SHARED = 0, 1
+ARL2_CACHE_NATIVE, ARL2_CACHE_E4M3 = 0, 1
 
 EXPORTED = (
     "arl2_create", "arl2_frame_forward", "arl2_frame_forward_host", "arl2_state_reset",
@@ -43,6 +51,9 @@ EXPORTED = (
     "arl2_kv_create", "arl2_kv_frame_forward", "arl2_kv_frame_forward_host", "arl2_kv_reset",
     "arl2_kv_frames", "arl2_kv_cache_get", "arl2_kv_cache_set", "arl2_kv_device_status", "arl2_kv_device_bytes",
     "arl2_kv_cache_bytes", "arl2_kv_kernel_launches", "arl2_kv_destroy",
+    "arl2_rotary_create", "arl2_rotary_apply", "arl2_rotary_destroy",
+    "arl2_paged_create", "arl2_paged_write", "arl2_paged_read", "arl2_paged_attend", "arl2_paged_forward",
+    "arl2_paged_device_status", "arl2_paged_device_bytes", "arl2_paged_kernel_launches", "arl2_paged_destroy",
 )
 NOALLOC_MAX_ELEMENTS = 1 << 22
 
@@ -67,6 +78,34 @@ class Arl2KvConfig(ctypes.Structure):
     ]
 
 
+class Arl2RotaryConfig(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int), ("axes", ctypes.c_int), ("axis_dim", ctypes.c_int * 4),
+        ("base", ctypes.c_double), ("pairs", ctypes.c_int), ("freqs", ctypes.c_int),
+    ]
+
+
+class Arl2PagedConfig(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+        ("pages", ctypes.c_int), ("page_tokens", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("format", ctypes.c_int), ("softmax_scale", ctypes.c_float), ("impl", ctypes.c_int),
+        ("max_ctas", ctypes.c_int),
+    ]
+
+
+class Arl2PagedPool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class Arl2PagedBatch(ctypes.Structure):
+    _fields_ = [
+        ("seqs", ctypes.c_int), ("tokens", ctypes.c_int), ("max_pages", ctypes.c_int), ("max_new", ctypes.c_int),
+        ("q_offsets", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -74,6 +113,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     H = ctypes.c_void_p
+    LL = ctypes.c_longlong
     sig = {
         "arl2_create": ([ctypes.POINTER(Arl2Config), P, ctypes.POINTER(H)], I),
         "arl2_frame_forward": ([H, P, P, P, P, P, I, P, P], I),
@@ -105,6 +145,18 @@ def _load() -> ctypes.CDLL:
         "arl2_kv_cache_bytes": ([H], S),
         "arl2_kv_kernel_launches": ([H], ctypes.c_ulonglong),
         "arl2_kv_destroy": ([H], None),
+        "arl2_rotary_create": ([ctypes.POINTER(Arl2RotaryConfig), ctypes.POINTER(H)], I),
+        "arl2_rotary_apply": ([H, I, I, P, I, P, LL, P, LL, I, P, LL, P, LL, I, P], I),
+        "arl2_rotary_destroy": ([H], None),
+        "arl2_paged_create": ([ctypes.POINTER(Arl2PagedConfig), P, ctypes.POINTER(H)], I),
+        "arl2_paged_write": ([H, P, P, P, LL, P, LL, P], I),
+        "arl2_paged_read": ([H, P, I, I, I, P, P, P, P, P, P], I),
+        "arl2_paged_attend": ([H, P, P, I, I, I, P, LL, P, P], I),
+        "arl2_paged_forward": ([H, P, P, H, P, I, I, I, P, LL, P, LL, P, LL, P, P, P], I),
+        "arl2_paged_device_status": ([H, P], I),
+        "arl2_paged_device_bytes": ([H], S),
+        "arl2_paged_kernel_launches": ([H], ctypes.c_ulonglong),
+        "arl2_paged_destroy": ([H], None),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -474,6 +526,319 @@ class TeacherLayer:
     def close(self) -> None:
         if getattr(self, "_h", None) is not None:
             _lib.arl2_kv_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def _dtype(t: torch.dtype) -> int:
+    if t not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    return ARL2_BF16 if t == torch.bfloat16 else ARL2_FP32
+
+
+def _head_rows(t, name, heads, d, dtype, device, tokens=None):
+    """A [tokens, heads, d] tensor whose tokens may be strided (a slice of a
+    joint qkv projection); returns it."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, {heads}, {d}]")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor of the layer's dtype and device")
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)
+                      or (t.shape[0] > 1 and t.stride(0) < heads * d)):
+        raise ValueError(f"{name} must have contiguous heads (tokens may be strided)")
+    return t
+
+
+def _token_stride(t) -> int:
+    # (the stride of a single token says nothing: dense)
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _table(t, name, shape, device):
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or any(
+            w is not None and w != n for w, n in zip(shape, t.shape)):
+        want = ["n" if w is None else w for w in shape]
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {want}")
+    return t
+
+
+def _new(like, shape, dtype, stream):
+    """An output of this call; the allocator is told when it is used on another
+    stream than the current one."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(stream, torch.cuda.Stream) and stream != torch.cuda.current_stream(like.device):
+        t.record_stream(stream)
+    return t
+
+
+class RotaryAxes:
+    """Rotary positions with up to four axes (arl2_rotary_* in the C ABI).
+
+    axis_dims: features of a head that each axis turns, in order (even; what
+    is left of head_dim passes through).  pairs: "adjacent" (2p, 2p + 1) or
+    "halves" (p, p + R/2).  freqs: "per_axis" (each axis runs through all
+    frequencies) or "shared" (one run over all axes' pairs).  A plan holds no
+    device memory and may be used on any device, stream and thread.
+    """
+
+    def __init__(self, head_dim: int, axis_dims, *, base: float = 10000.0, pairs: str = "adjacent",
+                 freqs: str = "per_axis"):
+        dims = [int(a) for a in axis_dims]
+        cfg = Arl2RotaryConfig(head_dim, len(dims), (ctypes.c_int * 4)(*dims[:4]), float(base),
+                               {"adjacent": ARL2_PAIRS_ADJACENT, "halves": ARL2_PAIRS_HALVES}[pairs],
+                               {"per_axis": ARL2_FREQS_PER_AXIS, "shared": ARL2_FREQS_SHARED}[freqs])
+        h = ctypes.c_void_p()
+        _check(_lib.arl2_rotary_create(ctypes.byref(cfg), ctypes.byref(h)), "arl2_rotary_create")
+        self._h = h
+        self.head_dim, self.axes = head_dim, len(dims)
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise RuntimeError("plan is closed")
+        return self._h
+
+    def apply(self, q, k, positions, *, inverse: bool = False, q_out=None, k_out=None, stream=None):
+        """(q, k) turned by positions (int32 [tokens, axes]): [tokens, heads, d]
+        each, k may be None.  inverse turns back, which is also the gradient.
+        q_out, k_out may be q, k (in place)."""
+        tokens, d = q.shape[0], self.head_dim
+        if not q.is_cuda:
+            raise ValueError("q must be a CUDA tensor")
+        dt = _dtype(q.dtype)
+        _head_rows(q, "q", q.shape[1] if q.dim() == 3 else 0, d, q.dtype, q.device)
+        _table(positions, "positions", (tokens, self.axes), q.device)
+        if q_out is None:
+            q_out = _new(q, q.shape, q.dtype, stream)
+        else:
+            _head_rows(q_out, "q_out", q.shape[1], d, q.dtype, q.device, tokens)
+        kh, ks, kos = 0, 0, 0
+        if k is None:
+            k_out = None
+        else:
+            kh = k.shape[1] if k.dim() == 3 else 0
+            _head_rows(k, "k", kh, d, q.dtype, q.device, tokens)
+            if k_out is None:
+                k_out = _new(k, k.shape, k.dtype, stream)
+            else:
+                _head_rows(k_out, "k_out", kh, d, q.dtype, q.device, tokens)
+            ks, kos = _token_stride(k), _token_stride(k_out)
+        if q.device.index != torch.cuda.current_device():
+            raise Arl2Error(-1, "arl2_rotary_apply: the current device is not the tensors'")
+        _check(_lib.arl2_rotary_apply(self.handle, dt, tokens, positions.data_ptr(), q.shape[1], q.data_ptr(),
+                                      _token_stride(q), q_out.data_ptr(), _token_stride(q_out), kh,
+                                      None if k is None else k.data_ptr(), ks,
+                                      None if k is None else k_out.data_ptr(), kos, 1 if inverse else 0,
+                                      _stream(stream)), "arl2_rotary_apply")
+        return q_out, k_out
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None:
+            _lib.arl2_rotary_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagedBatch:
+    """The sequences of a step and their chunks of new tokens (arl2_paged_batch).
+
+    q_offsets: int32 [seqs + 1], rows of each sequence's new tokens in the
+    token tensors; kv_lens: int32 [seqs], lengths with the new tokens;
+    page_table: int32 [seqs, max_pages].  max_new: the largest number of new
+    tokens of a sequence, if known (it picks the kernel).  The tensors are
+    read when the kernels run and are kept alive by this object.
+    """
+
+    def __init__(self, q_offsets, kv_lens, page_table, *, max_new: int = 0):
+        if not q_offsets.is_cuda:
+            raise ValueError("q_offsets must be a CUDA tensor")
+        self.device = q_offsets.device
+        seqs = int(kv_lens.shape[0])
+        _table(q_offsets, "q_offsets", (seqs + 1,), self.device)
+        _table(kv_lens, "kv_lens", (seqs,), self.device)
+        _table(page_table, "page_table", (seqs, None), self.device)
+        self.tensors = (q_offsets, kv_lens, page_table)
+        self.seqs, self.max_new, self.max_pages = seqs, int(max_new), int(page_table.shape[1])
+        self._c = {}
+
+    def struct(self, tokens: int):
+        c = self._c.get(tokens)
+        if c is None:
+            q, kv, pt = self.tensors
+            c = Arl2PagedBatch(self.seqs, tokens, self.max_pages, self.max_new, q.data_ptr(), kv.data_ptr(),
+                               pt.data_ptr())
+            self._c = {tokens: c}
+        return ctypes.byref(c)
+
+
+class PagedCache:
+    """A paged KV cache and the attention that reads it (arl2_paged_*).
+
+    The pools are tensors of this object: k_pages, v_pages [layers, pages,
+    kv_heads, page_tokens, d] in dtype or, with cache_format="e4m3", 8-bit
+    codes with k_scales, v_scales fp32 [layers, pages, kv_heads, page_tokens].
+    pool: existing ones instead, (k_pages, v_pages, k_scales, v_scales).
+    """
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, pages: int, page_tokens: int, *, layers: int = 1,
+                 dtype: torch.dtype = torch.bfloat16, cache_format: str = "native", softmax_scale: float = 0.0,
+                 impl: str = "auto", max_ctas: int = 0, pool=None, device=None, stream=None):
+        dt = _dtype(dtype)
+        e4m3 = {"native": False, "e4m3": True}[cache_format]
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.heads, self.head_dim, self.dtype, self.layers = (q_heads, kv_heads), head_dim, dtype, layers
+        cfg = Arl2PagedConfig(q_heads, kv_heads, head_dim, pages, page_tokens, dt,
+                              ARL2_CACHE_E4M3 if e4m3 else ARL2_CACHE_NATIVE, float(softmax_scale),
+                              {"auto": ARL2_IMPL_AUTO, "simt": ARL2_IMPL_SIMT}[impl], int(max_ctas))
+        shape = (layers, pages, kv_heads, page_tokens, head_dim)
+        store = torch.float8_e4m3fn if e4m3 else dtype
+        if pool is not None:
+            k, v, ks, vs = pool
+            for t, name, want, sh in ((k, "k_pages", store, shape), (v, "v_pages", store, shape),
+                                      (ks, "k_scales", torch.float32, shape[:4]),
+                                      (vs, "v_scales", torch.float32, shape[:4])):
+                if t is None and not e4m3 and name.endswith("scales"):
+                    continue
+                if t is None or (name.endswith("scales") and not e4m3) or t.dtype != want or tuple(t.shape) != sh \
+                        or not t.is_cuda or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous CUDA tensor {list(sh)} of {want}"
+                                     if e4m3 or not name.endswith("scales") else f"{name}: this format has none")
+            self.device = k.device
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(_lib.arl2_paged_create(ctypes.byref(cfg), _stream(stream), ctypes.byref(h)), "arl2_paged_create")
+        self._h = h
+        if pool is None:
+            k, v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else dtype, device=self.device).view(store)
+                    for _ in range(2))
+            ks, vs = (torch.zeros(shape[:4], device=self.device) if e4m3 else None for _ in range(2))
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k, v, ks, vs
+        self._pools = [Arl2PagedPool(k[i].data_ptr(), v[i].data_ptr(), None if ks is None else ks[i].data_ptr(),
+                                     None if vs is None else vs[i].data_ptr()) for i in range(layers)]
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise RuntimeError("cache is closed")
+        return self._h
+
+    def _pool(self, layer: int):
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer must be in 0..{self.layers - 1}")
+        return ctypes.byref(self._pools[layer])
+
+    def _batch(self, batch, tokens):
+        if batch.device != self.device:
+            raise ValueError("the batch's tables must be on the cache's device")
+        return batch.struct(tokens)
+
+    def _rows(self, t, name, kv, tokens=None):
+        return _head_rows(t, name, self.heads[kv], self.head_dim, self.dtype, self.device, tokens)
+
+    def _out(self, out, q, stream):
+        if out is None:
+            return _new(q, q.shape, q.dtype, stream)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+        return self._rows(out, "out", 0, q.shape[0])
+
+    def write(self, k, v, batch: PagedBatch, *, layer: int = 0, stream=None) -> None:
+        """The batch's new keys and values ([tokens, kv_heads, d]) into their pages."""
+        tokens = k.shape[0]
+        self._rows(k, "k", 1), self._rows(v, "v", 1, tokens)
+        _check(_lib.arl2_paged_write(self.handle, self._pool(layer), self._batch(batch, tokens), k.data_ptr(),
+                                     _token_stride(k), v.data_ptr(), _token_stride(v), _stream(stream)),
+               "arl2_paged_write")
+
+    def read(self, page_table, offsets, tokens: int, *, starts=None, layer: int = 0, k_out=None, v_out=None,
+             stream=None):
+        """(k, v) [tokens, kv_heads, d] read back: rows offsets[s] .. offsets[s + 1]
+        - 1 are sequence s's positions from starts[s] (default 0) on."""
+        seqs = page_table.shape[0]
+        _table(page_table, "page_table", (None, None), self.device)
+        _table(offsets, "offsets", (seqs + 1,), self.device)
+        if starts is not None:
+            _table(starts, "starts", (seqs,), self.device)
+        shape = (tokens, self.heads[1], self.head_dim)
+        outs = []
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is None:
+                t = _new(page_table, shape, self.dtype, stream)
+            elif not self._rows(t, name, 1, tokens).is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            outs.append(t)
+        _check(_lib.arl2_paged_read(self.handle, self._pool(layer), seqs, tokens, page_table.shape[1],
+                                    offsets.data_ptr(), None if starts is None else starts.data_ptr(),
+                                    page_table.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), _stream(stream)),
+               "arl2_paged_read")
+        return tuple(outs)
+
+    def attend(self, q, batch: PagedBatch, *, block: int = 1, window: int = 0, sinks: int = 0, layer: int = 0,
+               out=None, stream=None):
+        """Attention of the new tokens q [tokens, q_heads, d] over their
+        sequences' keys: up to the end of their own block of `block` tokens,
+        from `window` blocks back (0: from the start), the first `sinks` blocks
+        always.  Returns out [tokens, q_heads, d]; rows of no sequence are left
+        as they were."""
+        self._rows(q, "q", 0)
+        out = self._out(out, q, stream)
+        _check(_lib.arl2_paged_attend(self.handle, self._pool(layer), self._batch(batch, q.shape[0]), block, window,
+                                      sinks, q.data_ptr(), _token_stride(q), out.data_ptr(), _stream(stream)),
+               "arl2_paged_attend")
+        return out
+
+    def forward(self, q, k, v, batch: PagedBatch, *, rotary: RotaryAxes = None, positions=None, block: int = 1,
+                window: int = 0, sinks: int = 0, layer: int = 0, out=None, stream=None):
+        """One softmax layer's step: q and k turned by `rotary` at `positions`
+        (int32 [tokens, axes]; None: not turned), k and v written, then the
+        attention of the turned q.  Bit for bit apply, write and attend."""
+        tokens = q.shape[0]
+        self._rows(q, "q", 0), self._rows(k, "k", 1, tokens), self._rows(v, "v", 1, tokens)
+        turned = None
+        if rotary is not None:
+            if positions is None or rotary.head_dim != self.head_dim:
+                raise ValueError("rotary needs positions and the cache's head_dim")
+            _table(positions, "positions", (tokens, rotary.axes), self.device)
+            turned = _new(q, (tokens, sum(self.heads), self.head_dim), self.dtype, stream)
+        out = self._out(out, q, stream)
+        _check(_lib.arl2_paged_forward(self.handle, self._pool(layer), self._batch(batch, tokens),
+                                       None if rotary is None else rotary.handle,
+                                       None if rotary is None else positions.data_ptr(), block, window, sinks,
+                                       q.data_ptr(), _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
+                                       _token_stride(v), None if turned is None else turned.data_ptr(),
+                                       out.data_ptr(), _stream(stream)), "arl2_paged_forward")
+        return out
+
+    def device_status(self, stream=None) -> int:
+        """Synchronise and return the device status code: 0, ARL2_ERR_TIMEOUT,
+        or -1 if a batch's tables were wrong."""
+        return _lib.arl2_paged_device_status(self.handle, _stream(stream))
+
+    def device_bytes(self) -> int:
+        return int(_lib.arl2_paged_device_bytes(self.handle))
+
+    def kernel_launches(self) -> int:
+        return int(_lib.arl2_paged_kernel_launches(self.handle))
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None:
+            _lib.arl2_paged_destroy(self._h)
             self._h = None
 
     def __del__(self):

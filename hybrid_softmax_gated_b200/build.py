@@ -50,7 +50,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not verbose_ptxas and not _stale():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "--threads", "0", "-shared", "-Xcompiler", "-fPIC",
            "-cudart", "static", "-I", INCLUDE, "-I", CSRC, *sources(), "-o", tmp]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")

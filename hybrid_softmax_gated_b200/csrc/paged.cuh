@@ -1,0 +1,290 @@
+// Device code shared by the kernels that read the paged cache: the batch's
+// tables (checked before use), the keys a query tile sees, and the schedule
+// that splits the tiles' key blocks evenly over the CTAs.
+#pragma once
+
+#include "paged.h"
+
+#include <cuda_fp8.h>
+
+namespace arl2 {
+namespace paged {
+
+__device__ __forceinline__ void report(int* err, int bit) { atomicOr(err, bit); }
+
+// New tokens and length of sequence s; n = 0 if its entries are wrong.
+struct Seq {
+    int q0, n, total;
+};
+__device__ __forceinline__ Seq seq_at(const PagedSeqs& b, int page_log2, int s, int* err) {
+    const int q0 = b.q_off[s], q1 = b.q_off[s + 1], t = b.kv_len[s];
+    const bool bad = q0 < 0 || q1 < q0 || q1 > b.tokens || t < 0 || t > (b.max_pages << page_log2);
+    if (bad) {
+        report(err, kErrPagedTable);
+        return Seq{0, 0, 0};
+    }
+    return Seq{q0, q1 - q0, t};
+}
+
+// Page that holds key j of sequence s, or page 0 if the table's entry is
+// outside the pool: an address in bounds either way.
+__device__ __forceinline__ int page_at(const PagedSeqs& b, const PagedGeom& g, int s, int j, int* err) {
+    const int p = b.table[(size_t)s * b.max_pages + (j >> g.page_log2)];
+    if ((unsigned)p < (unsigned)g.pages) return p;
+    report(err, kErrPagedTable);
+    return 0;
+}
+
+// Row (page, head, slot) of key j in the pool's [pages][Hk][page] order.
+__device__ __forceinline__ size_t pool_row(const PagedGeom& g, int page, int head, int j) {
+    return (((size_t)page * g.Hk + head) << g.page_log2) + (j & ((1 << g.page_log2) - 1));
+}
+
+// Keys the query at position `at` sees: [0, sink) and [lo, end).
+struct Sight {
+    int end, lo, sink;
+};
+__device__ __forceinline__ Sight sight(const PagedMask& m, int at, int total) {
+    if (at < 0) return Sight{0, 0, 0};
+    const long long e = ((long long)(at / m.block) + 1) * m.block;
+    Sight s;
+    s.end = (int)(e < total ? e : total);
+    s.lo = 0;
+    s.sink = 0;
+    if (m.window) {
+        s.lo = (int)(e - m.window < 0 ? 0 : e - m.window);
+        s.sink = m.sinks < s.end ? m.sinks : s.end;
+    }
+    return s;
+}
+__device__ __forceinline__ bool sees(const Sight& s, int j) {
+    return j < s.end && (j >= s.lo || j < s.sink);
+}
+
+// Key blocks of KB keys that the tile of the new tokens [i0, i0 + n) sees:
+// blocks [0, ns) and [w0, w1).  Both ends of a query's window move right with
+// its position, so the first query gives the lower bound and the last the
+// upper one.
+struct Blocks {
+    int ns, w0, w1;
+    __device__ int count() const { return ns + w1 - w0; }
+    __device__ int at(int i) const { return i < ns ? i : w0 + i - ns; }
+};
+template <int KB>
+__device__ __forceinline__ Blocks blocks_of(const PagedMask& m, const Seq& q, int i0, int n) {
+    const int first = q.total - q.n + i0;
+    const Sight hi = sight(m, first + n - 1, q.total);
+    const Sight lo = sight(m, first < 0 ? 0 : first, q.total);
+    Blocks b;
+    b.w1 = (hi.end + KB - 1) / KB;
+    b.w0 = lo.lo / KB;
+    if (b.w0 > b.w1) b.w0 = b.w1;
+    b.ns = (hi.sink + KB - 1) / KB;
+    if (b.ns > b.w0) b.ns = b.w0;
+    return b;
+}
+
+// ---- schedule ---------------------------------------------------------------
+// A tile is up to TQ new tokens of one sequence with the G query heads of one
+// key head; a unit is one tile against one block of KB keys (a tile that sees
+// nothing still counts one: its zeros are written).  In the order (head,
+// sequence, tile, block), CTA c takes the units [c U / P, (c + 1) U / P) of
+// all U, P CTAs taking part.  A tile cut by such a border leaves one partial
+// in each CTA's piece of it; the last CTA to arrive merges them, in order.
+// Nobody waits for anybody.
+// Every CTA works this out from the device's tables: no host copy of the
+// lengths, no planning launch.
+struct PlanSmem {
+    int q_off[kPagedMaxSeqs + 1];
+    int total[kPagedMaxSeqs];
+    int tiles[kPagedMaxSeqs + 1];  // exclusive prefix of the sequences' tiles
+    long long warp_sum[32];
+    long long start_base;          // units of the head before the first tile
+    int start_seq, start_tile;
+};
+
+struct Cursor {
+    int h, s, t;       // head, sequence, tile of the sequence
+    long long base;    // the tile's first unit
+};
+
+struct Plan {
+    long long U, u0, u1;  // all units, this CTA's
+    int P;                // CTAs that take part
+    Cursor first;
+};
+
+// Exclusive prefix over the block's threads; *all gets the sum.
+__device__ __forceinline__ long long block_prefix(long long v, PlanSmem& ps, long long* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) ps.warp_sum[warp] = x;
+    __syncthreads();
+    long long before = 0, sum = 0;
+    for (int w = 0; w < warps; ++w) {
+        const long long y = ps.warp_sum[w];
+        if (w < warp) before += y;
+        sum += y;
+    }
+    __syncthreads();
+    *all = sum;
+    return before + x - v;
+}
+
+__device__ __forceinline__ Seq seq_of(const PlanSmem& ps, int s) {
+    return Seq{ps.q_off[s], ps.q_off[s + 1] - ps.q_off[s], ps.total[s]};
+}
+
+template <int KB>
+__device__ __forceinline__ int units_of(const PagedMask& m, const Seq& q, int t, int TQ) {
+    const int i0 = t * TQ;
+    const int c = blocks_of<KB>(m, q, i0, q.n - i0 < TQ ? q.n - i0 : TQ).count();
+    return c > 0 ? c : 1;
+}
+
+// The whole block.  grid CTAs; no CTA gets fewer than min_units units while
+// others have them (each cut costs a partial and its merge).
+template <int KB>
+__device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMask& m, int TQ, int min_units,
+                          PlanSmem& ps, int* err) {
+    const int N = blockDim.x, tid = threadIdx.x;
+    // tiles of each sequence
+    const int per = (b.S + N - 1) / N;
+    const int s0 = min(tid * per, b.S), s1 = min(s0 + per, b.S);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Seq q = seq_at(b, g.page_log2, s, err);
+        ps.q_off[s] = b.q_off[s];
+        ps.total[s] = q.total;
+        ps.tiles[s] = mine;
+        mine += (q.n + TQ - 1) / TQ;
+    }
+    if (tid == 0) ps.q_off[b.S] = b.q_off[b.S];
+    long long all;
+    const int before = (int)block_prefix(mine, ps, &all);
+    const int n_tiles = (int)all;
+    for (int s = s0; s < s1; ++s) ps.tiles[s] += before;
+    if (tid == 0) ps.tiles[b.S] = n_tiles;
+    __syncthreads();
+    Plan pl{};
+    if (n_tiles == 0) return pl;
+    // units of this thread's share of the tiles
+    const int tper = (n_tiles + N - 1) / N;
+    const int f0 = min(tid * tper, n_tiles), f1 = min(f0 + tper, n_tiles);
+    int s_first = 0;
+    if (f0 < f1) {  // last sequence whose first tile is <= f0 and that has tiles
+        int lo = 0, hi = b.S;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ps.tiles[mid] <= f0)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s_first = lo;
+    }
+    long long sum = 0;
+    for (int f = f0, s = s_first; f < f1; ++f) {
+        while (f >= ps.tiles[s + 1]) ++s;
+        sum += units_of<KB>(m, seq_of(ps, s), f - ps.tiles[s], TQ);
+    }
+    const long long pre = block_prefix(sum, ps, &all);
+    pl.U = all * g.Hk;
+    pl.P = gridDim.x;
+    if (pl.U < (long long)pl.P * min_units) pl.P = (int)((pl.U + min_units - 1) / min_units);
+    if ((int)blockIdx.x >= pl.P) return pl;
+    pl.u0 = pl.U * blockIdx.x / pl.P;
+    pl.u1 = pl.U * (blockIdx.x + 1) / pl.P;
+    const int h = (int)(pl.u0 / all);
+    const long long rem = pl.u0 - h * all;
+    if (sum > 0 && rem >= pre && rem < pre + sum) {
+        long long at = pre;
+        for (int f = f0, s = s_first; f < f1; ++f) {
+            while (f >= ps.tiles[s + 1]) ++s;
+            const int u = units_of<KB>(m, seq_of(ps, s), f - ps.tiles[s], TQ);
+            if (rem < at + u) {
+                ps.start_base = at;
+                ps.start_seq = s;
+                ps.start_tile = f - ps.tiles[s];
+                break;
+            }
+            at += u;
+        }
+    }
+    __syncthreads();
+    pl.first = Cursor{h, ps.start_seq, ps.start_tile, h * all + ps.start_base};
+    return pl;
+}
+
+// The tile under the cursor: its queries, blocks, and the CTA's piece of it.
+struct Piece {
+    Seq q;
+    int i0, n;          // first new token of the tile, tokens
+    Blocks blocks;
+    int units;          // of the whole tile
+    int b0, b1;         // the CTA's blocks of it: indices into blocks (b0 == b1: sees nothing)
+    int c0, c1;         // CTAs that share it
+};
+template <int KB>
+__device__ __forceinline__ Piece piece_at(const PagedMask& m, const PlanSmem& ps, const Plan& pl, const Cursor& c,
+                                          int TQ) {
+    Piece p;
+    p.q = seq_of(ps, c.s);
+    p.i0 = c.t * TQ;
+    p.n = min(TQ, p.q.n - p.i0);
+    p.blocks = blocks_of<KB>(m, p.q, p.i0, p.n);
+    const int count = p.blocks.count();
+    p.units = count > 0 ? count : 1;
+    const long long a = pl.u0 > c.base ? pl.u0 - c.base : 0;
+    const long long z = pl.u1 - c.base < p.units ? pl.u1 - c.base : p.units;
+    p.b0 = (int)a;
+    p.b1 = count > 0 ? (int)z : 0;
+    if (a == 0 && z == p.units) {
+        p.c0 = p.c1 = blockIdx.x;
+    } else {
+        p.c0 = (int)(((c.base + 1) * pl.P - 1) / pl.U);
+        p.c1 = (int)(((c.base + p.units) * pl.P - 1) / pl.U);
+    }
+    return p;
+}
+// To the next tile; false when it is not this CTA's.
+__device__ __forceinline__ bool advance(const PlanSmem& ps, const Plan& pl, const PagedSeqs& b, int units, Cursor& c) {
+    c.base += units;
+    if (c.base >= pl.u1) return false;
+    ++c.t;
+    if (c.t >= ps.tiles[c.s + 1] - ps.tiles[c.s]) {
+        c.t = 0;
+        do {
+            if (++c.s == b.S) {
+                c.s = 0;
+                ++c.h;
+            }
+        } while (ps.tiles[c.s + 1] == ps.tiles[c.s]);
+    }
+    return true;
+}
+// Where CTA c keeps its partial of the tile that starts at unit `base`: slot
+// 0 if the tile reaches back to or before the CTA's first unit, else 1 (a CTA
+// has at most one cut tile at each end).
+__device__ __forceinline__ int partial_slot(const Plan& pl, int c, long long base) {
+    return 2 * c + (pl.U * c / pl.P >= base ? 0 : 1);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x) {
+    return static_cast<float>(x);
+}
+template <>
+__device__ __forceinline__ float to_float<__nv_fp8_e4m3>(__nv_fp8_e4m3 x) {
+    return static_cast<float>(x);
+}
+__device__ __forceinline__ void store_as(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+}  // namespace paged
+}  // namespace arl2

@@ -354,6 +354,201 @@ unsigned long long arl2_kv_kernel_launches(const arl2_kv_handle* h);
 /* Release the handle (synchronises the device first); NULL is ignored. */
 void arl2_kv_destroy(arl2_kv_handle* h);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions with up to four axes (a video token's time, height and
+ * width; a text token's index).
+ *
+ * The first R = sum of axis_dim features of a head form R / 2 pairs; axis a
+ * owns axis_dim[a] / 2 consecutive ones, in order.  Pair p, the i-th of axis
+ * a, turns by the angle pos[n][a] * f_p:
+ *   (x, y) -> (x cos - y sin, x sin + y cos)
+ *   f_p = base^(-2 i / axis_dim[a])   (ARL2_FREQS_PER_AXIS)
+ *   f_p = base^(-2 p / R)             (ARL2_FREQS_SHARED)
+ * Features from R on pass through.  inverse turns by the opposite angle:
+ * the rotation's transpose, hence the gradient with respect to its input.
+ *
+ * An arl2_rotary is a host-side plan (the frequencies); it holds no device
+ * memory, is never written after its creation and may be used by several
+ * threads, streams and devices at once. */
+typedef enum { ARL2_PAIRS_ADJACENT = 0, ARL2_PAIRS_HALVES = 1 } arl2_pairs;
+typedef enum { ARL2_FREQS_PER_AXIS = 0, ARL2_FREQS_SHARED = 1 } arl2_freqs;
+
+typedef struct arl2_rotary arl2_rotary;
+
+typedef struct {
+    int head_dim;          /* d: 2..256                                       */
+    int axes;              /* columns of the positions: 1..4                  */
+    int axis_dim[4];       /* features of each axis: even, >= 0, sum in 2..d  */
+    double base;           /* >= 1                                            */
+    arl2_pairs pairs;      /* ADJACENT: features 2p, 2p + 1; HALVES: p, p + R/2 */
+    arl2_freqs freqs;
+} arl2_rotary_config;
+
+/* Create a plan.  Errors: INVALID_ARG, SHAPE, OOM.  No CUDA call. */
+arl2_status arl2_rotary_create(const arl2_rotary_config* cfg, arl2_rotary** out);
+
+/* Turn q [tokens][q_heads][d] and k [tokens][k_heads][d] (dtype, device; the
+ * heads of a token are contiguous, tokens are *_stride elements apart, 0 for
+ * dense) by positions (device int32 [tokens][axes], any sign) into q_out and
+ * k_out, in one launch.  An output may be its own input (in place) but not
+ * overlap any tensor otherwise.  q_heads or k_heads may be 0 (pointers
+ * unused then); tokens may be 0 (nothing to do).  The angle is formed as an
+ * exact product in 2^-64 turns and reduced before it is rounded, so far
+ * positions lose nothing.  Errors: INVALID_ARG, SHAPE, ALIGN (a pointer not
+ * aligned to its elements), CUDA. */
+arl2_status arl2_rotary_apply(const arl2_rotary* r, arl2_dtype dtype, int tokens, const int* positions,
+                              int q_heads, const void* q, long long q_stride, void* q_out,
+                              long long q_out_stride, int k_heads, const void* k, long long k_stride,
+                              void* k_out, long long k_out_stride, int inverse, cudaStream_t stream);
+
+/* Release the plan; NULL is ignored. */
+void arl2_rotary_destroy(arl2_rotary* r);
+
+/* ------------------------------------------------------------------------
+ * Paged KV cache and the attention that reads it.
+ *
+ * The teacher layer's cache (above) is one dense run of whole frames and all
+ * its streams are at the same frame.  Here every sequence (a video stream, a
+ * text) has its own length and its keys and values lie in pages of a pool
+ * that the caller owns, found through a page table, as they are or quantised
+ * to 8 bits.
+ *
+ * Pool of one layer:
+ *   k, v:             [pages][kv_heads][page_tokens][d], dtype or e4m3 codes
+ *   k_scale, v_scale: fp32 [pages][kv_heads][page_tokens] (e4m3 only)
+ * Key j of sequence s lies in page page_table[s][j / page_tokens], slot
+ * j % page_tokens.
+ *
+ * Quantised rows (one row: the d features of one token and head):
+ *   scale = max(max|x| / 448, 2^-126),  code = e4m3(x * (1 / scale))
+ * in fp32, codes rounded to nearest even; a row reads back as code * scale.
+ * A row that holds an infinity or NaN gets scale NaN and codes 0: it reads
+ * back as NaN.
+ *
+ * A batch names, for each of its sequences, the chunk of new tokens and the
+ * length with them; they are the sequence's last ones.  Row i of sequence s's
+ * new = q_offsets[s+1] - q_offsets[s] rows (rows q_offsets[s] on of the token
+ * tensors) has the position kv_lens[s] - new + i.  Rows at negative positions
+ * (a chunk padded on the left) and rows from q_offsets[seqs] on belong to no
+ * token: they are not written to the cache; the former's outputs are zeros,
+ * the latter's outputs are left as they were.
+ *
+ * The query at position p, with c = floor(p / block), sees the keys
+ *   j < min(kv_lens[s], (c + 1) block)   and
+ *   j >= (c + 1 - window) block  or  j < sinks block   (if window > 0)
+ * block = 1 is causal by token; block = tokens per frame is bidirectional
+ * within a frame and causal between frames (the teacher layer's mask).
+ * window counts blocks, the query's own among them; 0: no window.  sinks
+ * counts first blocks that stay visible.  A query that sees nothing gives
+ * zeros.  A key that a query does not see has no effect on it, whatever it
+ * holds.
+ *
+ * The lengths, offsets and tables are device memory, read when the kernels
+ * run: a captured graph may be replayed with other values in them.  They are
+ * checked there, before they are used as an address.  A sequence whose
+ * offsets are out of order or past `tokens`, whose length is negative or
+ * beyond max_pages pages, or a page number outside the pool sets the
+ * handle's error word: the sequence (or the page) is skipped, outputs of
+ * the sequence are undefined, and arl2_paged_device_status reports
+ * INVALID_ARG. */
+typedef enum { ARL2_CACHE_NATIVE = 0, ARL2_CACHE_E4M3 = 1 } arl2_cache_format;
+
+typedef struct arl2_paged_handle arl2_paged_handle;
+
+typedef struct {
+    int q_heads;           /* Hq: a multiple of kv_heads                      */
+    int kv_heads;          /* Hk >= 1; Hq / Hk <= 64                          */
+    int head_dim;          /* d: 128 for the bf16 tensor-core kernels; 1..128 SIMT */
+    int pages;             /* pages of a pool, >= 1                           */
+    int page_tokens;       /* 16, 32, 64, 128 or 256                          */
+    arl2_dtype dtype;      /* dtype of q, k, v and out                        */
+    arl2_cache_format format; /* NATIVE: the pool holds dtype                 */
+    float softmax_scale;   /* 0 selects 1/sqrt(d)                             */
+    arl2_impl impl;
+    int max_ctas;          /* as in arl2_config                               */
+} arl2_paged_config;
+
+/* One layer's pages (device memory of the caller, 16-byte aligned).  The
+ * same handle may serve the pools of many layers. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;        /* NULL unless the format is E4M3 */
+    float* v_scale;
+} arl2_paged_pool;
+
+typedef struct {
+    int seqs;              /* 0..1024                                         */
+    int tokens;            /* rows of the token tensors, >= 0                 */
+    int max_pages;         /* columns of page_table; max_pages * page_tokens
+                              <= 2^30                                         */
+    int max_new;           /* the largest number of new tokens of a sequence,
+                              or 0 if unknown: which kernel runs depends on
+                              it, no result does                              */
+    const int* q_offsets;  /* device int32 [seqs + 1], ascending              */
+    const int* kv_lens;    /* device int32 [seqs]                             */
+    const int* page_table; /* device int32 [seqs][max_pages]                  */
+} arl2_paged_batch;
+
+/* Create a handle on the current device (workspace and error word; no pool).
+ * Errors: INVALID_ARG, SHAPE, UNSUPPORTED (dtype/head_dim), OOM, CUDA. */
+arl2_status arl2_paged_create(const arl2_paged_config* cfg, cudaStream_t stream, arl2_paged_handle** out);
+
+/* Write the batch's new keys and values, k and v [tokens][kv_heads][d] dtype
+ * (tokens *_stride elements apart, 0 for dense), into their pages, quantised
+ * if the format says so.  Two rows of a batch must not share a slot.  Rows
+ * that go to the same pages as another sequence's (a shared prefix) are the
+ * caller's to keep apart. */
+arl2_status arl2_paged_write(arl2_paged_handle* h, const arl2_paged_pool* pool, const arl2_paged_batch* batch,
+                             const void* k, long long k_stride, const void* v, long long v_stride,
+                             cudaStream_t stream);
+
+/* Read keys and values back: rows offsets[s] .. offsets[s+1] - 1 of k_dst and
+ * v_dst ([tokens][kv_heads][d] dtype, dense) get sequence s's positions
+ * starts[s], starts[s] + 1, ... (starts NULL: from 0).  offsets: device int32
+ * [seqs + 1]; starts: device int32 [seqs]; page_table: [seqs][max_pages].
+ * Rows from offsets[seqs] on are left as they were. */
+arl2_status arl2_paged_read(arl2_paged_handle* h, const arl2_paged_pool* pool, int seqs, int tokens,
+                            int max_pages, const int* offsets, const int* starts, const int* page_table,
+                            void* k_dst, void* v_dst, cudaStream_t stream);
+
+/* Attention of the batch's new tokens, q [tokens][q_heads][d] (tokens
+ * q_stride elements apart, 0 for dense), over their sequences' keys; query
+ * head i reads key head i / (Hq / Hk).  out: [tokens][q_heads][d], dense, not
+ * overlapping q or the pool.  block >= 1, window >= 0, sinks >= 0 (see
+ * above).  With bf16 the softmax weights are rounded to bf16 before the
+ * product with v (times the key's scale, in E4M3), sums and statistics are
+ * fp32.  One launch. */
+arl2_status arl2_paged_attend(arl2_paged_handle* h, const arl2_paged_pool* pool, const arl2_paged_batch* batch,
+                              int block, int window, int sinks, const void* q, long long q_stride, void* out,
+                              cudaStream_t stream);
+
+/* One softmax layer's step: k and q turned by the plan (rotary NULL: not
+ * turned), k and v written to their pages, then the attention of the turned
+ * q.  The results, cache and output, are bit for bit those of
+ * arl2_rotary_apply, arl2_paged_write and arl2_paged_attend.  turned: device
+ * scratch of the caller, [tokens][q_heads + kv_heads][d] dtype, for the
+ * turned q and k (unused and may be NULL without rotary).  positions: as in
+ * arl2_rotary_apply. */
+arl2_status arl2_paged_forward(arl2_paged_handle* h, const arl2_paged_pool* pool, const arl2_paged_batch* batch,
+                               const arl2_rotary* rotary, const int* positions, int block, int window, int sinks,
+                               const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                               long long v_stride, void* turned, void* out, cudaStream_t stream);
+
+/* As arl2_device_status: TIMEOUT if a kernel gave up a bounded wait,
+ * INVALID_ARG if a batch's tables were wrong (see above), since the last
+ * check. */
+arl2_status arl2_paged_device_status(arl2_paged_handle* h, cudaStream_t stream);
+
+/* Device bytes the handle holds. */
+size_t arl2_paged_device_bytes(const arl2_paged_handle* h);
+
+/* Kernels this handle has enqueued since creation. */
+unsigned long long arl2_paged_kernel_launches(const arl2_paged_handle* h);
+
+/* Release the handle (synchronises the device first); NULL is ignored. */
+void arl2_paged_destroy(arl2_paged_handle* h);
+
 /* Static string for a status code. */
 const char* arl2_status_string(arl2_status s);
 
