@@ -148,7 +148,8 @@ arl2_status attend_now(arl2_paged_handle* h, const arl2_paged_pool* pool, const 
     const int max_new = b->max_new > 0 && b->max_new < b->tokens ? b->max_new : b->tokens;
     ++h->launches;
     const cudaError_t e =
-        arl2::launch_paged_simt(h->dtype == ARL2_BF16, h->e4m3, a, max_new, h->max_ctas, stream);
+        h->use_tc ? arl2::launch_paged_tc(h->e4m3, a, h->max_ctas, stream)
+                  : arl2::launch_paged_simt(h->dtype == ARL2_BF16, h->e4m3, a, max_new, h->max_ctas, stream);
     return e == cudaSuccess ? ARL2_OK : ARL2_ERR_CUDA;
 }
 
@@ -166,7 +167,7 @@ arl2_status arl2_paged_create(const arl2_paged_config* cfg, cudaStream_t stream,
     if (cfg->max_ctas < 0) return ARL2_ERR_INVALID_ARG;
     if (cfg->kv_heads < 1 || cfg->q_heads < 1 || cfg->q_heads > kMaxHeads || cfg->q_heads % cfg->kv_heads ||
         cfg->q_heads / cfg->kv_heads > kMaxGroup || cfg->head_dim < 1 || cfg->head_dim > kMaxHeadDim ||
-        cfg->pages < 1)
+        cfg->pages < 1 || (long long)cfg->pages * cfg->kv_heads >= 1ll << 31)
         return ARL2_ERR_SHAPE;
     int log2 = 4;
     while (log2 <= 8 && (1 << log2) != cfg->page_tokens) ++log2;
@@ -195,6 +196,7 @@ arl2_status arl2_paged_create(const arl2_paged_config* cfg, cudaStream_t stream,
     if (s == ARL2_OK) s = dalloc(h, &h->work.arrived, counters * sizeof(int));
     if (s == ARL2_OK) s = dalloc(h, &h->err, sizeof(int));
     if (s == ARL2_OK && arl2::paged_simt_init() != cudaSuccess) s = ARL2_ERR_CUDA;
+    if (s == ARL2_OK && use_tc && !arl2::paged_tc_init()) s = ARL2_ERR_CUDA;
     if (s == ARL2_OK && (cudaMemsetAsync(h->work.arrived, 0, counters * sizeof(int), stream) != cudaSuccess ||
                          cudaMemsetAsync(h->err, 0, sizeof(int), stream) != cudaSuccess))
         s = ARL2_ERR_CUDA;

@@ -86,8 +86,9 @@ __device__ __forceinline__ Blocks blocks_of(const PagedMask& m, const Seq& q, in
 
 // ---- schedule ---------------------------------------------------------------
 // A tile is up to TQ new tokens of one sequence with the G query heads of one
-// key head; a unit is one tile against one block of KB keys (a tile that sees
-// nothing still counts one: its zeros are written).  In the order (head,
+// key head; a unit is one tile, or one half of a tile of two (HT: tokens of a
+// half; HT = TQ: no halves), against one block of KB keys (a tile that sees
+// nothing still counts: its zeros are written).  In the order (head,
 // sequence, tile, block), CTA c takes the units [c U / P, (c + 1) U / P) of
 // all U, P CTAs taking part.  A tile cut by such a border leaves one partial
 // in each CTA's piece of it; the last CTA to arrive merges them, in order.
@@ -97,7 +98,6 @@ __device__ __forceinline__ Blocks blocks_of(const PagedMask& m, const Seq& q, in
 struct PlanSmem {
     int q_off[kPagedMaxSeqs + 1];
     int total[kPagedMaxSeqs];
-    int tiles[kPagedMaxSeqs + 1];  // exclusive prefix of the sequences' tiles
     long long warp_sum[32];
     long long start_base;          // units of the head before the first tile
     int start_seq, start_tile;
@@ -137,21 +137,26 @@ __device__ __forceinline__ long long block_prefix(long long v, PlanSmem& ps, lon
 }
 
 __device__ __forceinline__ Seq seq_of(const PlanSmem& ps, int s) {
-    return Seq{ps.q_off[s], ps.q_off[s + 1] - ps.q_off[s], ps.total[s]};
+    return ps.total[s] < 0 ? Seq{0, 0, 0} : Seq{ps.q_off[s], ps.q_off[s + 1] - ps.q_off[s], ps.total[s]};
 }
 
+// Units of a tile's block: 2 if the tile has more tokens than one half of it
+// holds (both halves work on every block), else 1.
+__device__ __forceinline__ int weight_of(const Seq& q, int t, int TQ, int HT) { return q.n - t * TQ > HT ? 2 : 1; }
+
 template <int KB>
-__device__ __forceinline__ int units_of(const PagedMask& m, const Seq& q, int t, int TQ) {
+__device__ __forceinline__ int units_of(const PagedMask& m, const Seq& q, int t, int TQ, int HT) {
     const int i0 = t * TQ;
     const int c = blocks_of<KB>(m, q, i0, q.n - i0 < TQ ? q.n - i0 : TQ).count();
-    return c > 0 ? c : 1;
+    return (c > 0 ? c : 1) * weight_of(q, t, TQ, HT);
 }
 
-// The whole block.  grid CTAs; no CTA gets fewer than min_units units while
+// The whole block.  tiles: kPagedMaxSeqs + 1 integers of shared memory for the
+// exclusive prefix of the sequences' tiles, free again afterwards.  grid CTAs; no CTA gets fewer than min_units units while
 // others have them (each cut costs a partial and its merge).
 template <int KB>
-__device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMask& m, int TQ, int min_units,
-                          PlanSmem& ps, int* err) {
+__device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMask& m, int TQ, int HT,
+                          int min_units, PlanSmem& ps, int* tiles, int* err) {
     const int N = blockDim.x, tid = threadIdx.x;
     // tiles of each sequence
     const int per = (b.S + N - 1) / N;
@@ -160,16 +165,16 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
     for (int s = s0; s < s1; ++s) {
         const Seq q = seq_at(b, g.page_log2, s, err);
         ps.q_off[s] = b.q_off[s];
-        ps.total[s] = q.total;
-        ps.tiles[s] = mine;
+        ps.total[s] = q.n > 0 ? q.total : -1;  // (-1: no rows, or wrong entries)
+        tiles[s] = mine;
         mine += (q.n + TQ - 1) / TQ;
     }
     if (tid == 0) ps.q_off[b.S] = b.q_off[b.S];
     long long all;
     const int before = (int)block_prefix(mine, ps, &all);
     const int n_tiles = (int)all;
-    for (int s = s0; s < s1; ++s) ps.tiles[s] += before;
-    if (tid == 0) ps.tiles[b.S] = n_tiles;
+    for (int s = s0; s < s1; ++s) tiles[s] += before;
+    if (tid == 0) tiles[b.S] = n_tiles;
     __syncthreads();
     Plan pl{};
     if (n_tiles == 0) return pl;
@@ -181,7 +186,7 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
         int lo = 0, hi = b.S;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (ps.tiles[mid] <= f0)
+            if (tiles[mid] <= f0)
                 lo = mid;
             else
                 hi = mid;
@@ -190,8 +195,8 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
     }
     long long sum = 0;
     for (int f = f0, s = s_first; f < f1; ++f) {
-        while (f >= ps.tiles[s + 1]) ++s;
-        sum += units_of<KB>(m, seq_of(ps, s), f - ps.tiles[s], TQ);
+        while (f >= tiles[s + 1]) ++s;
+        sum += units_of<KB>(m, seq_of(ps, s), f - tiles[s], TQ, HT);
     }
     const long long pre = block_prefix(sum, ps, &all);
     pl.U = all * g.Hk;
@@ -205,12 +210,12 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
     if (sum > 0 && rem >= pre && rem < pre + sum) {
         long long at = pre;
         for (int f = f0, s = s_first; f < f1; ++f) {
-            while (f >= ps.tiles[s + 1]) ++s;
-            const int u = units_of<KB>(m, seq_of(ps, s), f - ps.tiles[s], TQ);
+            while (f >= tiles[s + 1]) ++s;
+            const int u = units_of<KB>(m, seq_of(ps, s), f - tiles[s], TQ, HT);
             if (rem < at + u) {
                 ps.start_base = at;
                 ps.start_seq = s;
-                ps.start_tile = f - ps.tiles[s];
+                ps.start_tile = f - tiles[s];
                 break;
             }
             at += u;
@@ -227,23 +232,26 @@ struct Piece {
     int i0, n;          // first new token of the tile, tokens
     Blocks blocks;
     int units;          // of the whole tile
-    int b0, b1;         // the CTA's blocks of it: indices into blocks (b0 == b1: sees nothing)
+    int b0, b1;         // the CTA's blocks of it: indices into blocks (b0 == b1: none)
     int c0, c1;         // CTAs that share it
 };
 template <int KB>
 __device__ __forceinline__ Piece piece_at(const PagedMask& m, const PlanSmem& ps, const Plan& pl, const Cursor& c,
-                                          int TQ) {
+                                          int TQ, int HT) {
     Piece p;
     p.q = seq_of(ps, c.s);
     p.i0 = c.t * TQ;
     p.n = min(TQ, p.q.n - p.i0);
     p.blocks = blocks_of<KB>(m, p.q, p.i0, p.n);
     const int count = p.blocks.count();
-    p.units = count > 0 ? count : 1;
+    const int w = weight_of(p.q, c.t, TQ, HT);
+    p.units = (count > 0 ? count : 1) * w;
     const long long a = pl.u0 > c.base ? pl.u0 - c.base : 0;
     const long long z = pl.u1 - c.base < p.units ? pl.u1 - c.base : p.units;
-    p.b0 = (int)a;
-    p.b1 = count > 0 ? (int)z : 0;
+    // (a border inside a block of two units leaves the block to the CTA that
+    // has its first one)
+    p.b0 = count > 0 ? (int)(a + w - 1) / w : 0;
+    p.b1 = count > 0 ? (int)(z + w - 1) / w : 0;
     if (a == 0 && z == p.units) {
         p.c0 = p.c1 = blockIdx.x;
     } else {
@@ -253,18 +261,19 @@ __device__ __forceinline__ Piece piece_at(const PagedMask& m, const PlanSmem& ps
     return p;
 }
 // To the next tile; false when it is not this CTA's.
-__device__ __forceinline__ bool advance(const PlanSmem& ps, const Plan& pl, const PagedSeqs& b, int units, Cursor& c) {
+__device__ __forceinline__ bool advance(const PlanSmem& ps, const Plan& pl, const PagedSeqs& b, int TQ, int units,
+                                        Cursor& c) {
     c.base += units;
     if (c.base >= pl.u1) return false;
     ++c.t;
-    if (c.t >= ps.tiles[c.s + 1] - ps.tiles[c.s]) {
+    if (c.t * TQ >= seq_of(ps, c.s).n) {
         c.t = 0;
         do {
             if (++c.s == b.S) {
                 c.s = 0;
                 ++c.h;
             }
-        } while (ps.tiles[c.s + 1] == ps.tiles[c.s]);
+        } while (seq_of(ps, c.s).n <= 0);
     }
     return true;
 }

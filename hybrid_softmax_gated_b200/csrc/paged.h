@@ -51,7 +51,7 @@ struct PagedWork {
 };
 // Rows of partials the workspace holds per SM: two pieces per CTA, and a
 // kernel's CTAs per SM times its tile rows stay within this.
-constexpr int kPagedRowsPerSm = 256;
+constexpr int kPagedRowsPerSm = 512;
 
 struct PagedAttend {
     PagedGeom g;
@@ -76,5 +76,9 @@ cudaError_t launch_paged_read(bool bf16, bool e4m3, const PagedGeom& g, const Pa
 cudaError_t paged_simt_init();
 cudaError_t launch_paged_simt(bool bf16, bool e4m3, const PagedAttend& a, int max_new, int max_ctas,
                               cudaStream_t st);
+
+// bf16 tensors, head width 128, on the tensor cores (paged_tc.cu).
+bool paged_tc_init();
+cudaError_t launch_paged_tc(bool e4m3, const PagedAttend& a, int max_ctas, cudaStream_t st);
 
 }  // namespace arl2

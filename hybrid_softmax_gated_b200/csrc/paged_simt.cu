@@ -34,6 +34,7 @@ struct Smem {
     float ks[kKB], vs[kKB];
     long long row[kKB];  // pool row of each key of the block, -1: not there
     int last;
+    int tiles[kPagedMaxSeqs + 1];
     paged::PlanSmem plan;
 };
 
@@ -47,14 +48,14 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
     const PagedGeom& g = a.g;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int TQ = R / g.G;
-    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, 1, sm.plan, a.err);
+    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, TQ, 1, sm.plan, sm.tiles, a.err);
     if (pl.u1 == pl.u0) return;
     const T* q = static_cast<const T*>(a.q);
     const C* kp = static_cast<const C*>(a.pool.k);
     const C* vp = static_cast<const C*>(a.pool.v);
     paged::Cursor cur = pl.first;
     while (true) {
-        const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, TQ);
+        const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, TQ, TQ);
         const int rows = pc.n * g.G;
         __syncthreads();  // the previous tile is done with shared memory
         for (int i = tid; i < R * 128; i += kThreads) {
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
                 }
             }
         }
-        if (!paged::advance(sm.plan, pl, a.seqs, pc.units, cur)) break;
+        if (!paged::advance(sm.plan, pl, a.seqs, TQ, pc.units, cur)) break;
     }
 }
 

@@ -1,0 +1,918 @@
+// Attention of a batch's new tokens over the paged cache on the tensor cores
+// (tcgen05): bf16 queries and outputs, head width 128, pages of bf16 or of
+// e4m3 codes with one scale per token and head.
+//
+// A tile is up to 256 query rows (new tokens x the G query heads of one key
+// head), two halves of 128 rows = TMEM lanes, against blocks of 128 keys; the
+// schedule of paged.cuh splits all tiles' blocks evenly over one CTA per SM.
+// Softmax warpgroup w owns the S/P buffer w and the accumulator O_w:
+//   a tile of two halves: half w against every block of keys;
+//   a tile of one half (its rows fit 128): the half against every second
+//   block, so both warpgroups and the tensor core stay busy; O_0 and O_1 are
+//   combined at the end.
+// In both, item i of a piece (i = 0, 1, ...) belongs to warpgroup i & 1, and
+// the issue order is S_0, S_1, then P V_i followed by S_{i+2}: one
+// warpgroup's softmax runs beside the other's products.
+//
+// Roles: warp 0 loads (TMA: Q tiles, and each block's pages, found through
+// the page table, straight into one ring of K and V tiles), warp 1 issues the
+// products, warp 2 holds the TMEM, warp 3 clears the slots behind the last
+// key of a page (bf16 pages: what lies there may be NaN, and 0 x NaN is not
+// 0), warps 4-11 are the two softmax warpgroups and write the outputs.  With
+// codes warps 12-15 turn each staged block of codes into a bf16 tile: a code's
+// value is exact in bf16; the key's scale multiplies its scores, the value's
+// scale its weight, both in fp32.
+//
+// Softmax statistics, sums and accumulators are fp32.  The weights are
+// rounded to bf16, the type of the product with V; the sum they are divided
+// by is of the unrounded ones.  The running maximum moves only when it grows
+// by more than 2^8, which rescales O.
+//
+// Masked scores become -inf before the maximum: a weight of exactly 0.  What
+// a masked V row holds still enters 0 x v: if that is not finite, O is not,
+// and the rows it hit are computed again with plain loads of the keys they
+// see (repair_row): slow, and only for such rows.
+#include "paged.cuh"
+#include "ptx.cuh"
+#include "tma.h"
+
+#include <cmath>
+
+namespace arl2 {
+namespace {
+
+using ptx::kHalfBytes;
+using ptx::kTileBytes;
+
+constexpr int kRows = 128;  // rows of a half tile
+constexpr int kKB = 128;    // keys per block
+constexpr int kD = 128;
+constexpr int kCodeTile = kKB * kD;  // bytes of a block of codes
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // S/P buffers at 0, 128; O_0, O_1 at 256, 384
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kSoftmaxWarps = 8, kWgWarps = 4, kConvWarps = 4;
+constexpr int kDescs = 4;
+constexpr int kMinUnits = 2;
+
+template <bool kCodes>
+struct Cfg {
+    static constexpr int kThreads = kCodes ? 512 : 384;
+    static constexpr int kStages = kCodes ? 3 : 4;  // K/V tiles in the ring
+    static constexpr int kStaged = kCodes ? 3 : 1;  // blocks of codes on their way
+    // Registers per thread at launch (one CTA per SM) and after the split:
+    // the other warpgroups hand theirs to the two softmax warpgroups.
+    static constexpr int kRegsLaunch = kCodes ? 128 : 168;
+    static constexpr int kRegsLow = kCodes ? 72 : 96, kRegsConv = 72, kRegsHigh = kCodes ? 184 : 200;
+    static_assert(128 * kRegsLow + 256 * kRegsHigh + (kCodes ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch,
+                  "register split");
+};
+
+// What every role needs of a piece of work.
+struct Desc {
+    int done;
+    int s, h, row0, n;       // sequence, key head, first token row, tokens
+    int at0, total;          // position of the first token, keys of the sequence
+    int ns, w0, b0, b1;      // blocks (see Blocks), this CTA's
+    int pair;                // the tile has two halves
+    int c0, c1;              // CTAs that share the tile
+    long long base;
+    // first key of this CTA's block j
+    __device__ int key0(int j) const {
+        const int i = b0 + j;
+        return (i < ns ? i : w0 + i - ns) * kKB;
+    }
+};
+
+template <bool kCodes>
+struct __align__(1024) Smem {
+    uint8_t q[2][kTileBytes];
+    uint8_t kv[Cfg<kCodes>::kStages][kTileBytes];
+    uint8_t st[kCodes ? Cfg<kCodes>::kStaged : 1][kCodes ? kCodeTile : 16];
+    // scratch of the plan, then four slots of a block's key scales (times the
+    // softmax scale, log2 units) and value scales
+    __align__(16) int scratch[kPagedMaxSeqs + 4];
+    __device__ float* ks(int slot) { return reinterpret_cast<float*>(scratch) + slot * kKB; }
+    __device__ float* vs(int slot) { return reinterpret_cast<float*>(scratch) + (4 + slot) * kKB; }
+    uint64_t d_full[kDescs], d_empty[kDescs];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t kv_full[4], kv_empty[4];
+    uint64_t st_full[4], st_empty[4];
+    uint64_t v_tail;             // a ragged block of V has landed, its tail not cleared yet
+    uint64_t s_full[2];          // S of warpgroup w's item is in TMEM
+    uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the first / last 64 keys written
+    uint64_t pv_done[2];         // the piece's last P V of warpgroup w
+    uint64_t o_free;             // 8 warp arrivals per piece: O_0, O_1 read out
+    uint64_t ebar;               // 8 warp arrivals: the softmax warps meet
+    uint64_t drain;
+    float red_m[2][2][kRows], red_l[2][2][kRows];  // [piece & 1][warpgroup][row]
+    Desc desc[kDescs];
+    uint32_t tmem_base;
+    int abort;
+    int last;
+    paged::PlanSmem plan;
+};
+
+// A block of codes -> the two 128-byte-swizzled halves of a bf16 tile.  A code
+// s eeee mmm becomes the bf16 s 0000eeee mmm0000, its value times 2^-120
+// (subnormal codes are subnormal there too), and the product with 2^120 is
+// exact.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+    const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+    const uint32_t y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+    constexpr uint32_t k2p120 = 0x7b807b80u;  // 2^120 twice
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(k2p120));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k2p120));
+}
+
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// One output row again, by a whole warp, with plain loads: O = sum over the
+// keys it sees of the blocks [b0, b1) of exp2(score - m) v, lane l holding
+// features 4 l .. 4 l + 3.  bf16 pages.
+__device__ __noinline__ float4 repair_row(const PagedAttend& a, const Desc& d, int token, int head, float m,
+                                          float scale_log2) {
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16* q =
+        static_cast<const __nv_bfloat16*>(a.q) + (long long)(d.row0 + token) * a.q_stride + head * kD + 4 * lane;
+    float qf[4];
+    for (int c = 0; c < 4; ++c) qf[c] = paged::to_float(q[c]);
+    const paged::Sight see = paged::sight(a.mask, d.at0 + token, d.total);
+    const float base = m == -INFINITY ? 0.f : m;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int bi = d.b0; bi < d.b1; ++bi) {
+        const int key0 = d.key0(bi - d.b0);
+        for (int j = key0; j < key0 + kKB; ++j) {
+            if (!paged::sees(see, j)) continue;
+            const int page = a.seqs.table[(size_t)d.s * a.seqs.max_pages + (j >> a.g.page_log2)];
+            if ((unsigned)page >= (unsigned)a.g.pages) continue;  // (reported by the loader)
+            const size_t at = paged::pool_row(a.g, page, d.h, j) * kD + 4 * lane;
+            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.pool.k) + at;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool.v) + at;
+            float s = 0.f;
+            for (int c = 0; c < 4; ++c) s = fmaf(qf[c], paged::to_float(k[c]), s);
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const float p = ptx::ex2(fmaf(s, scale_log2, -base));
+            for (int c = 0; c < 4; ++c) acc[c] = fmaf(p, paged::to_float(v[c]), acc[c]);
+        }
+    }
+    return make_float4(acc[0], acc[1], acc[2], acc[3]);
+}
+
+template <bool kCodes>
+__global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttend a,
+                    float scale_log2) {
+    using C = Cfg<kCodes>;
+    extern __shared__ uint8_t smem_raw[];
+    Smem<kCodes>& sm = *reinterpret_cast<Smem<kCodes>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                        ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PagedGeom& g = a.g;
+    volatile int* abort = &sm.abort;
+    const int no_abort = 0;
+    if (threadIdx.x == 0) {
+        auto init = [](uint64_t* b, int n) { ptx::mbar_init(ptx::smem_u32(b), n); };
+        for (int i = 0; i < kDescs; ++i) {
+            init(&sm.d_full[i], 1);
+            init(&sm.d_empty[i], 1 + kSoftmaxWarps + (kCodes ? kConvWarps : 1));
+        }
+        for (int i = 0; i < 4; ++i) {
+            init(&sm.kv_full[i], kCodes ? kConvWarps : 1);
+            init(&sm.kv_empty[i], 1);
+            init(&sm.st_full[i], 1);
+            init(&sm.st_empty[i], kConvWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            init(&sm.q_full[i], 1);
+            init(&sm.q_empty[i], 1);
+            init(&sm.s_full[i], 1);
+            init(&sm.p_half[i], kWgWarps);
+            init(&sm.p_full[i], kWgWarps);
+            init(&sm.pv_done[i], 1);
+        }
+        init(&sm.v_tail, 1);
+        init(&sm.o_free, kSoftmaxWarps);
+        init(&sm.ebar, kSoftmaxWarps);
+        init(&sm.drain, 1);
+        sm.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc(ptx::smem_u32(&sm.tmem_base), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    const int HT = kRows / g.G, TQ = 2 * HT;  // tokens of a half tile, of a tile
+    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, HT, kMinUnits, sm.plan, sm.scratch, a.err);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    auto fail = [&]() {
+        atomicOr(a.err, kErrPagedTimeout);
+        *abort = 1;
+    };
+    // bounded wait with a warp-uniform result (every role runs as whole warps)
+    auto wwait = [&](uint64_t* bar, uint32_t parity) {
+        return ptx::mbar_wait_warp(ptx::smem_u32(bar), parity, abort, kWaitLimitNs);
+    };
+    auto arrive1 = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(bar));
+    };
+    // piece si's descriptor, copied; its slot is free again once all have
+    auto get_desc = [&](int si, Desc& d) -> bool {
+        if (!wwait(&sm.d_full[si % kDescs], (si / kDescs) & 1)) return false;
+        d = sm.desc[si % kDescs];
+        arrive1(&sm.d_empty[si % kDescs]);
+        return true;
+    };
+
+    if (warp < 4) ptx::setmaxnreg_dec<C::kRegsLow>();
+    if (warp == 0) {
+        // ------------------------------------------------------ loader --
+        ptx::tma_prefetch_desc(&tm_q);
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+        paged::Cursor cur = pl.first;
+        const int page_tokens = 1 << g.page_log2;
+        const int per_block = page_tokens < kKB ? kKB >> g.page_log2 : 1;  // pages of a block
+        const int absent = g.pages * g.Hk;                                // reads as zeros
+        int cnt = 0, qn = 0, tails = 0;
+        bool ok = true, more = pl.u1 > pl.u0;
+        for (int si = 0; ok; ++si) {
+            const int slot = si % kDescs;
+            if (si >= kDescs && !wwait(&sm.d_empty[slot], (si / kDescs - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            if (!more) {
+                if (lane == 0) sm.desc[slot].done = 1;
+                arrive1(&sm.d_full[slot]);
+                break;
+            }
+            const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, TQ, HT);
+            const bool pair = pc.n > HT;
+            const int at0 = pc.q.total - pc.q.n + pc.i0;
+            if (lane == 0)
+                sm.desc[slot] = Desc{0,          cur.s,        cur.h,        pc.q.q0 + pc.i0, pc.n, at0,
+                                     pc.q.total, pc.blocks.ns, pc.blocks.w0, pc.b0,           pc.b1, pair,
+                                     pc.c0,      pc.c1,        cur.base};
+            arrive1(&sm.d_full[slot]);
+            const int n = pc.b1 - pc.b0;
+            if (n > 0) {
+                for (int t = 0; ok && t < (pair ? 2 : 1); ++t, ++qn) {
+                    const int qs = qn & 1;
+                    if (qn >= 2 && !wwait(&sm.q_empty[qs], ((qn >> 1) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = ptx::smem_u32(&sm.q_full[qs]), dst = ptx::smem_u32(sm.q[qs]);
+                    ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(HT * g.G) * 256u);
+                    const int row = pc.q.q0 + pc.i0 + t * HT;
+                    ptx::tma_load_4d_w(dst, &tm_q, 0, cur.h * g.G, row, 0, bar);
+                    ptx::tma_load_4d_w(dst + kHalfBytes, &tm_q, 64, cur.h * g.G, row, 0, bar);
+                }
+                // keys that some query of the tile sees: [0, see_sink) and [see_lo, see_end)
+                const paged::Sight last = paged::sight(a.mask, at0 + pc.n - 1, pc.q.total);
+                const int see_lo = paged::sight(a.mask, at0 < 0 ? 0 : at0, pc.q.total).lo;
+                // this lane's page of piece block j: its place in the pool, or absent
+                auto look_up = [&](int j) -> int {
+                    if (j >= n || lane >= per_block) return absent;
+                    const int k0 = pc.blocks.at(pc.b0 + j) * kKB + (lane << g.page_log2);
+                    const int span = page_tokens < kKB ? page_tokens : kKB;
+                    if (k0 >= last.end || (k0 + span <= see_lo && k0 >= last.sink)) return absent;
+                    const int p = a.seqs.table[(size_t)cur.s * a.seqs.max_pages + (k0 >> g.page_log2)];
+                    if ((unsigned)p < (unsigned)g.pages) return p * g.Hk + cur.h;
+                    paged::report(a.err, kErrPagedTable);
+                    return absent;
+                };
+                auto load = [&](int j, int place, const CUtensorMap* tm, bool is_v) -> bool {
+                    const int key0 = pc.blocks.at(pc.b0 + j) * kKB;
+                    const int slot0 = key0 & (page_tokens - 1);
+                    if constexpr (kCodes) {
+                        const int s = cnt % C::kStaged;
+                        if (cnt >= C::kStaged && !wwait(&sm.st_empty[s], (cnt / C::kStaged - 1) & 1)) return false;
+                        const uint32_t bar = ptx::smem_u32(&sm.st_full[s]);
+                        ptx::mbar_arrive_expect_tx_w(bar, kCodeTile);
+                        __syncwarp();
+                        if (lane < per_block)
+                            ptx::tma_load_4d(ptx::smem_u32(sm.st[s]) + (uint32_t)(lane << g.page_log2) * 128u, tm, 0,
+                                             slot0, place, 0, bar);
+                    } else {
+                        const int s = cnt % C::kStages;
+                        if (cnt >= C::kStages && !wwait(&sm.kv_empty[s], (cnt / C::kStages - 1) & 1)) return false;
+                        uint64_t* full = &sm.kv_full[s];
+                        if (is_v && j == n - 1 && key0 + kKB > pc.q.total) {
+                            full = &sm.v_tail;  // (the previous use has been waited for by warp 3)
+                            ++tails;
+                        }
+                        const uint32_t bar = ptx::smem_u32(full);
+                        ptx::mbar_arrive_expect_tx_w(bar, kTileBytes);
+                        __syncwarp();
+                        if (lane < per_block) {
+                            const uint32_t dst = ptx::smem_u32(sm.kv[s]) + (uint32_t)(lane << g.page_log2) * 128u;
+                            ptx::tma_load_4d(dst, tm, 0, slot0, place, 0, bar);
+                            ptx::tma_load_4d(dst + kHalfBytes, tm, 64, slot0, place, 0, bar);
+                        }
+                    }
+                    __syncwarp();
+                    ++cnt;
+                    return true;
+                };
+                // K runs one item ahead of V for each warpgroup: the order in
+                // which the products take them
+                int p0 = look_up(0), p1 = look_up(1), p2 = look_up(2);
+                if (ok) ok = load(0, p0, &tm_k, false);
+                if (ok && !pair && n > 1) ok = load(1, p1, &tm_k, false);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int p3 = look_up(j + 3);
+                    ok = load(j, p0, &tm_v, true);
+                    const int next = j + (pair ? 1 : 2);
+                    if (ok && next < n) ok = load(next, pair ? p1 : p2, &tm_k, false);
+                    p0 = p1;
+                    p1 = p2;
+                    p2 = p3;
+                }
+            }
+            more = paged::advance(sm.plan, pl, a.seqs, TQ, pc.units, cur);
+        }
+        if (!ok) fail();
+        // the last loads of each ring have landed before exit
+        if constexpr (kCodes) {
+            for (int i = cnt > C::kStaged ? cnt - C::kStaged : 0; i < cnt; ++i)
+                ptx::mbar_wait_bounded(ptx::smem_u32(&sm.st_full[i % C::kStaged]), (i / C::kStaged) & 1, &no_abort,
+                                       kWaitLimitNs);
+        } else {
+            if (tails)
+                ptx::mbar_wait_bounded(ptx::smem_u32(&sm.v_tail), (tails - 1) & 1, &no_abort, kWaitLimitNs);
+            for (int i = cnt > C::kStages ? cnt - C::kStages : 0; i < cnt; ++i)
+                ptx::mbar_wait_bounded(ptx::smem_u32(&sm.kv_full[i % C::kStages]), (i / C::kStages) & 1, &no_abort,
+                                       kWaitLimitNs);
+        }
+        for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i)
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, &no_abort, kWaitLimitNs);
+    } else if (warp == 1) {
+        // ------------------------------------------------------ issuer --
+        const uint32_t idesc_s = ptx::idesc_bf16_f32(kRows, kKB, false, false);
+        const uint32_t idesc_pv = ptx::idesc_bf16_f32(kRows, kD, false, true);  // V: MN-major
+        int cnt = 0, qn = 0, pieces = 0;
+        uint32_t p_par = 0;
+        bool ok = true;
+        for (int si = 0; ok; ++si) {
+            Desc d;
+            if (!get_desc(si, d)) {
+                ok = false;
+                break;
+            }
+            if (d.done) break;
+            const int n = d.b1 - d.b0;
+            if (n <= 0) continue;
+            const bool pair = d.pair != 0;
+            const int N = pair ? 2 * n : n;
+            const int q0 = qn, nq = pair ? 2 : 1;
+            for (int t = 0; ok && t < nq; ++t, ++qn) ok = wwait(&sm.q_full[qn & 1], (qn >> 1) & 1);
+            int ks = 0, vs = 0;  // ring stages of the K and V tile in use
+            // the ring's next tile, in the order it was loaded
+            auto take = [&](int& s) -> bool {
+                s = cnt % C::kStages;
+                if (!wwait(&sm.kv_full[s], (cnt / C::kStages) & 1)) return false;
+                ++cnt;
+                return true;
+            };
+            const bool keep = pair;  // a tile serves two items
+            auto s_ready = [&](int i) -> bool { return (keep && (i & 1)) || take(ks); };
+            auto s_issue = [&](int i) {
+                ptx::tc_fence_after();
+                const uint32_t q_s = ptx::smem_u32(sm.q[(q0 + (pair ? i & 1 : 0)) & 1]);
+                const uint32_t k_s = ptx::smem_u32(sm.kv[ks]);
+                ptx::umma_ss8_kk(tmem + kColS + (uint32_t)(i & 1) * kKB, ptx::kmajor_desc(q_s, 0),
+                                 ptx::kmajor_desc(k_s, 0), idesc_s, 0u);
+                ptx::umma_commit_w(ptx::smem_u32(&sm.s_full[i & 1]));
+                if (!keep || (i & 1)) ptx::umma_commit_w(ptx::smem_u32(&sm.kv_empty[ks]));
+                if (i == N - 1)
+                    for (int t = 0; t < nq; ++t) ptx::umma_commit_w(ptx::smem_u32(&sm.q_empty[(q0 + t) & 1]));
+            };
+            for (int i = 0; ok && i < 2 && i < N; ++i) {
+                ok = s_ready(i);
+                if (ok) s_issue(i);
+            }
+            // O_0 and O_1 are free once the previous piece has been read out
+            if (ok && pieces > 0) ok = wwait(&sm.o_free, (pieces - 1) & 1);
+            ++pieces;
+            for (int i = 0; ok && i < N; ++i) {
+                const int w = i & 1;
+                const uint32_t par = (p_par >> w) & 1;
+                p_par ^= 1u << w;
+                if (!keep || w == 0) ok = take(vs);
+                ok = ok && wwait(&sm.p_half[w], par);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t p_t = tmem + kColS + (uint32_t)w * kKB;
+                const uint32_t o_t = tmem + kColO + (uint32_t)w * kD;
+                const uint32_t v_s = ptx::smem_u32(sm.kv[vs]);
+                // O_w += P V in two halves of 64 keys: the first runs while
+                // the softmax warps work on the second's P
+                ptx::umma_ts4_mn(o_t, p_t, ptx::mnmajor_desc(v_s, 0), idesc_pv, i >= 2 ? 1u : 0u);
+                const bool next = i + 2 < N;
+                ok = (!next || s_ready(i + 2)) && wwait(&sm.p_full[w], par);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                ptx::umma_ts4_mn(o_t, p_t + 32u, ptx::mnmajor_desc(v_s, 4), idesc_pv, 1u);
+                if (!keep || w == 1) ptx::umma_commit_w(ptx::smem_u32(&sm.kv_empty[vs]));
+                if (next)
+                    s_issue(i + 2);
+                else
+                    ptx::umma_commit_w(ptx::smem_u32(&sm.pv_done[w]));
+            }
+        }
+        if (!ok) {
+            fail();
+            // nothing may still run on the tensor cores when TMEM is released
+            ptx::umma_commit_w(ptx::smem_u32(&sm.drain));
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sm.drain), 0, &no_abort, kWaitLimitNs);
+        }
+    } else if (warp == 3) {
+        // ----------------------------------- slots behind the last key --
+        if constexpr (!kCodes) {
+            int cnt = 0, tails = 0;
+            bool ok = true;
+            for (int si = 0; ok; ++si) {
+                Desc d;
+                if (!get_desc(si, d)) {
+                    ok = false;
+                    break;
+                }
+                if (d.done) break;
+                const int n = d.b1 - d.b0;
+                if (n <= 0) continue;
+                cnt += 2 * n;
+                const int key0 = d.key0(n - 1);
+                if (key0 + kKB <= d.total) continue;
+                ok = wwait(&sm.v_tail, tails & 1);
+                ++tails;
+                if (!ok) break;
+                const int s = (cnt - 1) % C::kStages;  // the piece's last tile
+                const int first = d.total > key0 ? d.total - key0 : 0;
+                for (int half = 0; half < 2; ++half)
+                    for (int at = first * 128 + lane * 16; at < (int)kHalfBytes; at += 512)
+                        *reinterpret_cast<uint4*>(sm.kv[s] + half * kHalfBytes + at) = make_uint4(0u, 0u, 0u, 0u);
+                ptx::fence_proxy_async_smem();
+                arrive1(&sm.kv_full[s]);
+            }
+            if (!ok) fail();
+        }
+    } else if (warp >= 12) {
+        // --------------------------------------- codes -> bf16 tiles --
+        if constexpr (kCodes) {
+            ptx::setmaxnreg_dec<C::kRegsConv>();
+            const int cw = warp - 12, tid = threadIdx.x - 384;  // tid: a key of the block
+            int cnt = 0, blk = 0;
+            bool ok = true;
+            for (int si = 0; ok; ++si) {
+                Desc d;
+                if (!get_desc(si, d)) {
+                    ok = false;
+                    break;
+                }
+                if (d.done) break;
+                const int n = d.b1 - d.b0;
+                if (n <= 0) continue;
+                const bool pair = d.pair != 0;
+                const int end = paged::sight(a.mask, d.at0 + d.n - 1, d.total).end;
+                auto scales = [&](int j) -> float2 {  // of this thread's key of piece block j
+                    if (j >= n) return make_float2(0.f, 0.f);
+                    const int key = d.key0(j) + tid;
+                    if (key >= end) return make_float2(0.f, 0.f);
+                    const int p = a.seqs.table[(size_t)d.s * a.seqs.max_pages + (key >> g.page_log2)];
+                    if ((unsigned)p >= (unsigned)g.pages) return make_float2(0.f, 0.f);  // (reported by the loader)
+                    const size_t row = paged::pool_row(g, p, d.h, key);
+                    return make_float2(a.pool.ks[row], a.pool.vs[row]);
+                };
+                auto convert = [&](int j, bool is_k, float2 sc) -> bool {
+                    const int f = cnt % C::kStaged, s = cnt % C::kStages;
+                    if (!wwait(&sm.st_full[f], (cnt / C::kStaged) & 1)) return false;
+                    if (cnt >= C::kStages && !wwait(&sm.kv_empty[s], (cnt / C::kStages - 1) & 1)) return false;
+                    if (is_k) {  // (K waits for the V of three tiles before: the slot's readers are done)
+                        sm.ks((blk + j) & 3)[tid] = sc.x * scale_log2;
+                        sm.vs((blk + j) & 3)[tid] = sc.y;
+                    }
+                    const uint8_t* from = sm.st[f];
+                    const uint32_t to = ptx::smem_u32(sm.kv[s]);
+                    const int c = lane & 7;  // this lane's 16 features
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = cw * 32 + i * 4 + (lane >> 3);
+                        const uint4 u = *reinterpret_cast<const uint4*>(from + r * 128 + c * 16);
+                        uint32_t y[8];
+                        codes_to_bf16(u.x, y[0], y[1]);
+                        codes_to_bf16(u.y, y[2], y[3]);
+                        codes_to_bf16(u.z, y[4], y[5]);
+                        codes_to_bf16(u.w, y[6], y[7]);
+                        // (the lanes of the second half swap their two stores:
+                        // eight lanes then cover all banks)
+                        const bool sw = c >= 4;
+                        const int c0 = 2 * c + (sw ? 1 : 0), c1 = 2 * c + (sw ? 0 : 1);
+                        ptx::st_shared_v4(to + ptx::tile_chunk_offset(r, c0), sw ? y[4] : y[0], sw ? y[5] : y[1],
+                                          sw ? y[6] : y[2], sw ? y[7] : y[3]);
+                        ptx::st_shared_v4(to + ptx::tile_chunk_offset(r, c1), sw ? y[0] : y[4], sw ? y[1] : y[5],
+                                          sw ? y[2] : y[6], sw ? y[3] : y[7]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    arrive1(&sm.kv_full[s]);
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.st_empty[f]));
+                    ++cnt;
+                    return true;
+                };
+                const float2 s0 = scales(0);
+                float2 s1 = scales(1), s2 = scales(2);
+                ok = convert(0, true, s0);
+                if (ok && !pair && n > 1) ok = convert(1, true, s1);
+                for (int j = 0; ok && j < n; ++j) {
+                    const float2 s3 = scales(j + 3);
+                    ok = convert(j, false, s3);
+                    const int next = j + (pair ? 1 : 2);
+                    if (ok && next < n) ok = convert(next, true, pair ? s1 : s2);
+                    s1 = s2;
+                    s2 = s3;
+                }
+                blk += n;
+            }
+            if (!ok) fail();
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------ softmax, epilogue --
+        ptx::setmaxnreg_inc<C::kRegsHigh>();
+        const int wg = (warp - 4) >> 2;                // S/P buffer and accumulator
+        const int row = ((warp & 3) << 5) + lane;      // row of the half tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t sbuf = tmem + lane_base + kColS + (uint32_t)wg * kKB;
+        const uint32_t obuf = tmem + lane_base + kColO + (uint32_t)wg * kD;
+        uint32_t s_par = 0, e_uses = 0, pv_par = 0;
+        int blk = 0;
+        bool ok = true;
+        // all 8 softmax warps meet (arrive, then a bounded wait)
+        auto meet = [&]() -> bool {
+            arrive1(&sm.ebar);
+            return wwait(&sm.ebar, (e_uses++) & 1);
+        };
+        const float2 sl2 = make_float2(scale_log2, scale_log2);
+        for (int si = 0; ok; ++si) {
+            // (read where it is, and given back at the piece's end: registers are short)
+            ok = wwait(&sm.d_full[si % kDescs], (si / kDescs) & 1);
+            if (!ok) break;
+            const Desc& d = sm.desc[si % kDescs];
+            if (d.done) break;
+            const int n = d.b1 - d.b0;
+            const bool pair = d.pair != 0;
+            // this thread's row
+            const int in_half = row / g.G;
+            const int token = (pair ? wg * HT : 0) + in_half;
+            const int head = d.h * g.G + row - in_half * g.G;
+            const bool valid = in_half < HT && token < d.n;
+            const bool busy = __any_sync(0xffffffffu, valid);  // else nobody reads this warp's rows
+            const paged::Sight see = valid ? paged::sight(a.mask, d.at0 + token, d.total) : paged::Sight{0, 0, 0};
+            float m_run = -INFINITY, l_run = 0.f;
+            const int step = pair ? 1 : 2, j0 = pair ? 0 : wg;
+            for (int j = j0; j < n; j += step) {
+                ok = wwait(&sm.s_full[wg], s_par);
+                s_par ^= 1u;
+                if (!ok) break;
+                if (!busy) {
+                    arrive1(&sm.p_half[wg]);
+                    arrive1(&sm.p_full[wg]);
+                    continue;
+                }
+                ptx::tc_fence_after();
+                uint32_t raw[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ptx::tmem_ld32(sbuf + (uint32_t)c * 32, raw[c]);
+                const int key0 = d.key0(j);
+                // nothing of the block is hidden from this row (rows of no query: never mind)
+                const bool open = !valid || (key0 + kKB <= see.end && (key0 >= see.lo || key0 + kKB <= see.sink));
+                const bool masked = __any_sync(0xffffffffu, !open);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ptx::reg_fence(raw[c]);
+                float x[128];
+#pragma unroll
+                for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(raw[i >> 5][i & 31]);
+                const float* kscale = sm.ks((blk + j) & 3);
+                const float* vscale = sm.vs((blk + j) & 3);
+                if constexpr (kCodes) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float4 k4 = *reinterpret_cast<const float4*>(kscale + 4 * i);
+                        const float2 lo = ptx::mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(k4.x, k4.y));
+                        const float2 hi = ptx::mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(k4.z, k4.w));
+                        x[4 * i] = lo.x, x[4 * i + 1] = lo.y, x[4 * i + 2] = hi.x, x[4 * i + 3] = hi.y;
+                    }
+                }
+                if (masked) {
+                    const int e = see.end - key0, lo = see.lo - key0, si2 = see.sink - key0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t seen = bits_below(e - 32 * k) & (~bits_below(lo - 32 * k) | bits_below(si2 - 32 * k));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[32 * k + i] = (seen >> i) & 1u ? x[32 * k + i] : -INFINITY;
+                    }
+                }
+                // row max: 3-input max tree
+                float m16[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    m16[i] = ptx::max3(ptx::max3(x[8 * i], x[8 * i + 1], x[8 * i + 2]),
+                                       ptx::max3(x[8 * i + 3], x[8 * i + 4], x[8 * i + 5]),
+                                       fmaxf(x[8 * i + 6], x[8 * i + 7]));
+                float m4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    m4[i] = ptx::max3(m16[4 * i], m16[4 * i + 1], fmaxf(m16[4 * i + 2], m16[4 * i + 3]));
+                float mx = ptx::max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                if constexpr (!kCodes) mx *= scale_log2;
+                const float m_new = fmaxf(m_run, mx);
+                const bool need = m_new > m_run + kRescaleLog2;
+                const float m_use = need ? m_new : m_run;
+                const float corr = need ? ptx::ex2(m_run - m_new) : 1.f;
+                const float base = m_use == -INFINITY ? 0.f : m_use;  // nothing seen yet: weights 2^-inf
+                const float2 nm = make_float2(-base, -base);
+                float2 sum4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+                uint32_t pk[64];
+                // P (bf16 pairs) over the first 64 columns of the S buffer, in
+                // two halves of 64 keys, each handed to the issuer when stored
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int i = 32 * hf; i < 32 * hf + 32; ++i) {
+                        const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
+                        float2 e;
+                        if constexpr (kCodes)
+                            e = ptx::add2(xi, nm);
+                        else
+                            e = ptx::fma2(xi, sl2, nm);
+                        float2 p;
+                        p.x = ptx::ex2(e.x);
+                        p.y = ptx::ex2(e.y);
+                        sum4[i & 3] = ptx::add2(sum4[i & 3], p);
+                        if constexpr (kCodes) {
+                            // (a hidden value's scale may be anything)
+                            const float2 v2 = *reinterpret_cast<const float2*>(vscale + 2 * i);
+                            float2 w = ptx::mul2(p, v2);
+                            if (masked) {
+                                w.x = xi.x == -INFINITY ? 0.f : w.x;
+                                w.y = xi.y == -INFINITY ? 0.f : w.y;
+                            }
+                            pk[i] = ptx::pack_bf16x2(w.x, w.y);
+                        } else {
+                            pk[i] = ptx::pack_bf16x2(p.x, p.y);
+                        }
+                    }
+                    if (hf == 0 && j > j0 && __any_sync(0xffffffffu, need)) {
+                        // rescale O_w before this item's P V adds to it: S of
+                        // this item was committed after the P V of the previous
+                        // one, so that is done
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32(obuf + (uint32_t)c * 32, o);
+                            ptx::tmem_wait_ld();
+                            ptx::reg_fence(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                            ptx::tmem_st32(obuf + (uint32_t)c * 32, o);
+                        }
+                    }
+                    ptx::tmem_st32_u(sbuf + 32u * hf, pk + 32 * hf);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    arrive1(hf == 0 ? &sm.p_half[wg] : &sm.p_full[wg]);
+                }
+                const float2 s2 = ptx::add2(ptx::add2(sum4[0], sum4[1]), ptx::add2(sum4[2], sum4[3]));
+                l_run = l_run * corr + (s2.x + s2.y);
+                m_run = m_use;
+            }
+            if (!ok) break;
+            blk += n;
+            // ------------------------------------------------ epilogue --
+            const bool has[2] = {n > 0, pair ? n > 0 : n > 1};
+            // the row's statistics over the piece, and what O_0 and O_1 count
+            float m = m_run, l = l_run, f0 = 1.f, f1 = 1.f;
+            if (!pair) {
+                float(&rm)[2][kRows] = sm.red_m[si & 1];
+                float(&rl)[2][kRows] = sm.red_l[si & 1];
+                rm[wg][row] = m_run;
+                rl[wg][row] = l_run;
+                ok = meet();
+                if (!ok) break;
+                const float m0 = rm[0][row], m1 = rm[1][row];
+                m = fmaxf(m0, m1);
+                // (weights without a maximum are NaN or none)
+                f0 = m0 == -INFINITY ? 1.f : ptx::ex2(m0 - m);
+                f1 = m1 == -INFINITY ? 1.f : ptx::ex2(m1 - m);
+                l = f0 * rl[0][row] + f1 * rl[1][row];
+            }
+            for (int w = 0; ok && w < 2; ++w) {
+                if (!has[w]) continue;
+                if (!pair || w == wg) ok = wwait(&sm.pv_done[w], (pv_par >> w) & 1);
+                pv_par ^= 1u << w;
+            }
+            if (!ok) break;
+            ptx::tc_fence_after();
+            // this thread's columns of the row: all of O_wg, or half of both
+            const int col0 = pair ? 0 : 64 * wg, chunks = pair ? 4 : 2;
+            const bool use0 = pair ? wg == 0 && n > 0 : has[0], use1 = pair ? wg == 1 && n > 0 : has[1];
+            const bool cut = d.c0 != d.c1;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                 ((size_t)(d.row0 + token) * g.Hq + head) * kD;
+            const int slot = cut ? paged::partial_slot(pl, blockIdx.x, d.base) : 0;
+            const int half = pair ? wg : 0;
+            float4* part = reinterpret_cast<float4*>(a.work.o) + (size_t)slot * 2 * 32 * kRows + half * 32 * kRows + row;
+            float zero = 0.f;
+            if (busy) {
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t o0[32], o1[32];
+                    const uint32_t at = tmem + lane_base + kColO + (uint32_t)(col0 + 32 * c);
+                    if (use0) ptx::tmem_ld32(at, o0);
+                    if (use1) ptx::tmem_ld32(at + kD, o1);
+                    ptx::tmem_wait_ld();
+                    ptx::reg_fence(o0);
+                    ptx::reg_fence(o1);
+                    float acc[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float x0 = use0 ? f0 * __uint_as_float(o0[i]) : 0.f;
+                        acc[i] = use1 ? fmaf(f1, __uint_as_float(o1[i]), x0) : x0;
+                        zero = fmaf(acc[i], 0.f, zero);
+                    }
+                    if (valid && cut) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            part[(size_t)(col0 / 4 + 8 * c + i) * kRows] =
+                                make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                    } else if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = ptx::pack_bf16x2(acc[8 * i + 2 * e] * inv, acc[8 * i + 2 * e + 1] * inv);
+                            *reinterpret_cast<uint4*>(out + col0 + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (cut && valid && (pair || wg == 0)) a.work.ml[(size_t)slot * 2 * kRows + half * kRows + row] = make_float2(m, l);
+            }
+            ptx::tc_fence_before();
+            if (n > 0) arrive1(&sm.o_free);
+            if constexpr (!kCodes) {
+                uint32_t hurt = __ballot_sync(0xffffffffu, valid && !(zero == 0.f));
+                __syncwarp();
+                while (hurt) {
+                    const int src = __ffs(hurt) - 1;
+                    hurt &= hurt - 1;
+                    const int r_token = __shfl_sync(0xffffffffu, token, src);
+                    const int r_head = __shfl_sync(0xffffffffu, head, src);
+                    const float r_m = __shfl_sync(0xffffffffu, m, src);
+                    const float r_inv = __shfl_sync(0xffffffffu, inv, src);
+                    const float4 o = repair_row(a, d, r_token, r_head, r_m, scale_log2);
+                    if (4 * lane >= col0 && 4 * lane < col0 + 32 * chunks) {
+                        if (cut) {
+                            part[lane * kRows + src - lane] = o;
+                        } else {
+                            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) +
+                                                ((size_t)(d.row0 + r_token) * g.Hq + r_head) * kD + 4 * lane;
+                            *reinterpret_cast<uint2*>(to) = make_uint2(ptx::pack_bf16x2(o.x * r_inv, o.y * r_inv),
+                                                                       ptx::pack_bf16x2(o.z * r_inv, o.w * r_inv));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!cut) {
+                arrive1(&sm.d_empty[si % kDescs]);
+                continue;
+            }
+            // The last CTA to arrive merges the tile's partials, in order.
+            __threadfence();
+            ok = meet();
+            if (!ok) break;
+            if (threadIdx.x == 128) {
+                const int arrived = atomicAdd(a.work.arrived + d.c0, 1);
+                sm.last = arrived == d.c1 - d.c0;
+                if (sm.last) a.work.arrived[d.c0] = 0;
+                __threadfence();
+            }
+            ok = meet();
+            if (!ok) break;
+            if (sm.last && valid) {
+                __threadfence();
+                const float2* ml = a.work.ml + half * kRows + row;
+                auto slot_of = [&](int c) { return (size_t)paged::partial_slot(pl, c, d.base); };
+                float mm = -INFINITY, ll = 0.f;
+                for (int c = d.c0; c <= d.c1; ++c) mm = fmaxf(mm, __ldcg(ml + slot_of(c) * 2 * kRows).x);
+                for (int c = d.c0; c <= d.c1; ++c) {
+                    const float2 x = __ldcg(ml + slot_of(c) * 2 * kRows);
+                    ll += x.x == -INFINITY ? x.y : x.y * ptx::ex2(x.x - mm);
+                }
+                const float r = ll == 0.f ? 0.f : 1.f / ll;
+                const float4* po = reinterpret_cast<const float4*>(a.work.o) + (size_t)half * 32 * kRows +
+                                   (size_t)(col0 / 4) * kRows + row;
+#pragma unroll 1
+                for (int c8 = 0; c8 < chunks; ++c8) {
+                    float acc[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+                    for (int c = d.c0; c <= d.c1; ++c) {
+                        const float mc = __ldcg(ml + slot_of(c) * 2 * kRows).x;
+                        const float w = mc == -INFINITY ? 1.f : ptx::ex2(mc - mm);
+                        const float4* from = po + slot_of(c) * 2 * 32 * kRows + (size_t)(8 * c8) * kRows;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 x = __ldcg(from + (size_t)i * kRows);
+                            acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
+                            acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
+                            acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
+                            acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = ptx::pack_bf16x2(acc[8 * i + 2 * e] * r, acc[8 * i + 2 * e + 1] * r);
+                        *reinterpret_cast<uint4*>(out + col0 + 32 * c8 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            arrive1(&sm.d_empty[si % kDescs]);
+        }
+        if (!ok) fail();
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <bool kCodes>
+bool ready() {
+    const auto kernel = paged_tc_kernel<kCodes>;
+    static_assert(sizeof(Smem<kCodes>) + 1024 <= 232448, "shared memory");
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<kCodes>) + 1024) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    // the warpgroups' register split needs the launch count it was sized for
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != Cfg<kCodes>::kRegsLaunch) {
+        cudaGetLastError();
+        return false;
+    }
+    return true;
+}
+
+template <bool kCodes>
+cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int page = 1 << a.g.page_log2, box = page < kKB ? page : kKB;
+    const long long outer = (long long)a.g.pages * a.g.Hk;
+    const int HT = kRows / a.g.G;
+    CUtensorMap q, k, v;
+    if (!tma_encode_head_rows(&q, a.q, a.g.Hq, a.seqs.tokens, a.q_stride, a.g.G, HT) ||
+        !tma_encode_pages(&k, a.pool.k, kCodes, page, outer, box) ||
+        !tma_encode_pages(&v, a.pool.v, kCodes, page, outer, box))
+        return cudaErrorInvalidValue;
+    const int grid = max_ctas > 0 && max_ctas < sms ? max_ctas : sms;
+    static_assert(2 * 2 * kRows <= kPagedRowsPerSm, "workspace rows");
+    paged_tc_kernel<kCodes><<<grid, Cfg<kCodes>::kThreads, sizeof(Smem<kCodes>) + 1024, st>>>(
+        q, k, v, a, a.scale * 1.4426950408889634f);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool paged_tc_init() { return tma_available() && ready<false>() && ready<true>(); }
+
+cudaError_t launch_paged_tc(bool e4m3, const PagedAttend& a, int max_ctas, cudaStream_t st) {
+    return e4m3 ? launch<true>(a, max_ctas, st) : launch<false>(a, max_ctas, st);
+}
+
+}  // namespace arl2

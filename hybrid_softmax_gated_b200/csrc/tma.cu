@@ -75,6 +75,27 @@ bool tma_encode_tiles(CUtensorMap* m, const void* p, int outer) {
     return encode4(m, p, dims, strides, box);
 }
 
+bool tma_encode_pages(CUtensorMap* m, const void* p, bool codes, int page, long long outer, int box_rows) {
+    if (!tma_available() || outer < 1 || outer >= (1ll << 31)) return false;
+    const cuuint64_t row = codes ? 128 : 256;
+    const cuuint64_t dims[4] = {128, (cuuint64_t)page, (cuuint64_t)outer, 1};
+    const cuuint64_t strides[3] = {row, row * page, row * page * outer};
+    const cuuint32_t box[4] = {codes ? 128u : 64u, (cuuint32_t)box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tma_encode_head_rows(CUtensorMap* m, const void* p, int heads, long long tokens, long long stride, int box_heads,
+                          int box_tokens) {
+    const cuuint64_t dims[4] = {128, (cuuint64_t)heads, (cuuint64_t)tokens, 1};
+    const cuuint64_t strides[3] = {256, (cuuint64_t)stride * 2, (cuuint64_t)stride * 2 * tokens};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1};
+    return encode4(m, p, dims, strides, box);
+}
+
 TokenMapCache::TokenMapCache(const Dims& dm) : dm_(dm), entries_(new (std::nothrow) Entry[kSlots]) {
     if (entries_)
         for (int i = 0; i < kSlots; ++i) entries_[i].p = nullptr;

@@ -32,6 +32,18 @@ bool tma_encode_rows_2d(CUtensorMap* m, const void* p, long long inner, long lon
 // innermost dimension contiguous): dims {128, 128, outer}; box {64, 128, 1}.
 bool tma_encode_tiles(CUtensorMap* m, const void* p, int outer);
 
+// A pool of pages [outer][page][128] (outer = pages x heads), bf16 or (codes)
+// 8-bit: dims {128, page, outer, 1}; box {64, box_rows, 1, 1} with the
+// 128-byte swizzle, or for codes {128, box_rows, 1, 1} without one.  An outer
+// coordinate past the end reads as zeros.
+bool tma_encode_pages(CUtensorMap* m, const void* p, bool codes, int page, long long outer, int box_rows);
+
+// Tokens of a [tokens][heads][128] bf16 tensor, `stride` elements apart:
+// dims {128, heads, tokens, 1}; box {64, box_heads, box_tokens, 1}, tokens past
+// the end read as zeros.
+bool tma_encode_head_rows(CUtensorMap* m, const void* p, int heads, long long tokens, long long stride, int box_heads,
+                          int box_tokens);
+
 // Direct-mapped cache of token-tensor maps keyed by pointer (one per
 // handle; its dimensions never change).
 class TokenMapCache {
