@@ -101,16 +101,18 @@ struct __align__(1024) Smem {
     uint64_t st_full[4], st_empty[4];
     uint64_t v_tail;             // a ragged block of V has landed, its tail not cleared yet
     uint64_t s_full[2];          // S of warpgroup w's item is in TMEM
-    uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the first / last 64 keys written
+    uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the last / first 64 keys written
     uint64_t pv_done[2];         // the piece's last P V of warpgroup w
     uint64_t o_free;             // 8 warp arrivals per piece: O_0, O_1 read out
     uint64_t ebar;               // 8 warp arrivals: the softmax warps meet
     uint64_t drain;
+    float ones[kCodes ? kKB : 4];
     float red_m[2][2][kRows], red_l[2][2][kRows];  // [piece & 1][warpgroup][row]
     Desc desc[kDescs];
     uint32_t tmem_base;
     int abort;
     int last;
+    paged::Plan pl;
     paged::PlanSmem plan;
 };
 
@@ -129,6 +131,20 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
 
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Row `row` of warpgroup wg's half tile: token of the tile and query head.
+struct RowOf {
+    int token, head;
+    bool valid;
+};
+__device__ __forceinline__ RowOf row_of(const Desc& d, int row, int wg, int G, int HT) {
+    const int i = row / G;
+    RowOf r;
+    r.token = (d.pair ? wg * HT : 0) + i;
+    r.head = d.h * G + row - i * G;
+    r.valid = i < HT && r.token < d.n;
+    return r;
 }
 
 // One output row again, by a whole warp, with plain loads: O = sum over the
@@ -204,12 +220,14 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
+    if (kCodes && threadIdx.x < kKB) sm.ones[threadIdx.x] = 1.f;
     if (warp == 2) {
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
     const int HT = kRows / g.G, TQ = 2 * HT;  // tokens of a half tile, of a tile
     const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, HT, kMinUnits, sm.plan, sm.scratch, a.err);
+    if (threadIdx.x == 0) sm.pl = pl;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -415,17 +433,17 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 ok = ok && wwait(&sm.p_half[w], par);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t p_t = tmem + kColS + (uint32_t)w * kKB;
+                const uint32_t p_t = tmem + kColS + (uint32_t)w * kKB + 64u;
                 const uint32_t o_t = tmem + kColO + (uint32_t)w * kD;
                 const uint32_t v_s = ptx::smem_u32(sm.kv[vs]);
-                // O_w += P V in two halves of 64 keys: the first runs while
-                // the softmax warps work on the second's P
-                ptx::umma_ts4_mn(o_t, p_t, ptx::mnmajor_desc(v_s, 0), idesc_pv, i >= 2 ? 1u : 0u);
+                // O_w += P V in two halves of 64 keys, the last 64 first: they
+                // run while the softmax warps work on the other half's P
+                ptx::umma_ts4_mn(o_t, p_t + 32u, ptx::mnmajor_desc(v_s, 4), idesc_pv, i >= 2 ? 1u : 0u);
                 const bool next = i + 2 < N;
                 ok = (!next || s_ready(i + 2)) && wwait(&sm.p_full[w], par);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                ptx::umma_ts4_mn(o_t, p_t + 32u, ptx::mnmajor_desc(v_s, 4), idesc_pv, 1u);
+                ptx::umma_ts4_mn(o_t, p_t, ptx::mnmajor_desc(v_s, 0), idesc_pv, 1u);
                 if (!keep || w == 1) ptx::umma_commit_w(ptx::smem_u32(&sm.kv_empty[vs]));
                 if (next)
                     s_issue(i + 2);
@@ -572,13 +590,14 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             if (d.done) break;
             const int n = d.b1 - d.b0;
             const bool pair = d.pair != 0;
-            // this thread's row
-            const int in_half = row / g.G;
-            const int token = (pair ? wg * HT : 0) + in_half;
-            const int head = d.h * g.G + row - in_half * g.G;
-            const bool valid = in_half < HT && token < d.n;
-            const bool busy = __any_sync(0xffffffffu, valid);  // else nobody reads this warp's rows
-            const paged::Sight see = valid ? paged::sight(a.mask, d.at0 + token, d.total) : paged::Sight{0, 0, 0};
+            // what this thread's row sees (a row of no query: whatever there is)
+            paged::Sight see{1 << 30, 0, 0};
+            bool busy;  // else nobody reads this warp's rows
+            {
+                const RowOf r = row_of(d, row, wg, g.G, HT);
+                if (r.valid) see = paged::sight(a.mask, d.at0 + r.token, d.total);
+                busy = __any_sync(0xffffffffu, r.valid);
+            }
             float m_run = -INFINITY, l_run = 0.f;
             const int step = pair ? 1 : 2, j0 = pair ? 0 : wg;
             for (int j = j0; j < n; j += step) {
@@ -591,52 +610,77 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                     continue;
                 }
                 ptx::tc_fence_after();
-                uint32_t raw[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) ptx::tmem_ld32(sbuf + (uint32_t)c * 32, raw[c]);
                 const int key0 = d.key0(j);
-                // nothing of the block is hidden from this row (rows of no query: never mind)
-                const bool open = !valid || (key0 + kKB <= see.end && (key0 >= see.lo || key0 + kKB <= see.sink));
+                // nothing of the block is hidden from this row
+                const bool open = key0 + kKB <= see.end && (key0 >= see.lo || key0 + kKB <= see.sink);
                 const bool masked = __any_sync(0xffffffffu, !open);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) ptx::reg_fence(raw[c]);
-                float x[128];
-#pragma unroll
-                for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(raw[i >> 5][i & 31]);
-                const float* kscale = sm.ks((blk + j) & 3);
-                const float* vscale = sm.vs((blk + j) & 3);
-                if constexpr (kCodes) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float4 k4 = *reinterpret_cast<const float4*>(kscale + 4 * i);
-                        const float2 lo = ptx::mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(k4.x, k4.y));
-                        const float2 hi = ptx::mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(k4.z, k4.w));
-                        x[4 * i] = lo.x, x[4 * i + 1] = lo.y, x[4 * i + 2] = hi.x, x[4 * i + 3] = hi.y;
-                    }
-                }
                 if (masked) {
-                    const int e = see.end - key0, lo = see.lo - key0, si2 = see.sink - key0;
+                    // hidden scores become -inf where they are: a pass of its
+                    // own, for the few blocks at the mask's edges, costs the
+                    // other blocks no registers
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[32];
+                        ptx::tmem_ld32(sbuf + (uint32_t)c * 32, y);
+                        const int k = key0 + 32 * c;
+                        const uint32_t seen = bits_below(see.end - k) & (~bits_below(see.lo - k) | bits_below(see.sink - k));
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence(y);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t seen = bits_below(e - 32 * k) & (~bits_below(lo - 32 * k) | bits_below(si2 - 32 * k));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[32 * k + i] = (seen >> i) & 1u ? x[32 * k + i] : -INFINITY;
+                        for (int i = 0; i < 32; ++i) {
+                            // (after the key's scale, which may be anything where the key is hidden)
+                            if constexpr (kCodes)
+                                y[i] = __float_as_uint(__uint_as_float(y[i]) * sm.ks((blk + j) & 3)[32 * c + i]);
+                            y[i] = (seen >> i) & 1u ? y[i] : 0xff800000u;
+                        }
+                        ptx::tmem_st32(sbuf + (uint32_t)c * 32, y);
                     }
+                    ptx::tmem_wait_st();
                 }
-                // row max: 3-input max tree
-                float m16[16];
+                const float* kscale = kCodes && masked ? sm.ones : sm.ks((blk + j) & 3);
+                const float* vscale = sm.vs((blk + j) & 3);
+                // columns 32 c .. 32 c + 31 of the scores (codes: times the key scales)
+                auto scaled = [&](uint32_t(&y)[32], int c) {
+                    ptx::reg_fence(y);
+                    if constexpr (kCodes) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    m16[i] = ptx::max3(ptx::max3(x[8 * i], x[8 * i + 1], x[8 * i + 2]),
-                                       ptx::max3(x[8 * i + 3], x[8 * i + 4], x[8 * i + 5]),
-                                       fmaxf(x[8 * i + 6], x[8 * i + 7]));
-                float m4[4];
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(kscale + 32 * c + 4 * i);
+                            const float2 lo = ptx::mul2(make_float2(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])),
+                                                        make_float2(k4.x, k4.y));
+                            const float2 hi = ptx::mul2(make_float2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])),
+                                                        make_float2(k4.z, k4.w));
+                            y[4 * i] = __float_as_uint(lo.x), y[4 * i + 1] = __float_as_uint(lo.y);
+                            y[4 * i + 2] = __float_as_uint(hi.x), y[4 * i + 3] = __float_as_uint(hi.y);
+                        }
+                    }
+                };
+                auto top = [](const uint32_t(&y)[32]) {  // 3-input max tree
+                    float m8[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    m4[i] = ptx::max3(m16[4 * i], m16[4 * i + 1], fmaxf(m16[4 * i + 2], m16[4 * i + 3]));
-                float mx = ptx::max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                    for (int i = 0; i < 4; ++i) {
+                        auto f = [&](int k) { return __uint_as_float(y[8 * i + k]); };
+                        m8[i] = ptx::max3(ptx::max3(f(0), f(1), f(2)), ptx::max3(f(3), f(4), f(5)), fmaxf(f(6), f(7)));
+                    }
+                    return ptx::max3(m8[0], m8[1], fmaxf(m8[2], m8[3]));
+                };
+                // The row's maximum, of all 128 scores; the last 64 stay in
+                // registers, the first 64 are loaded again: all of them would
+                // not fit beside the rest.
+                uint32_t ya[32], yb[32], yc[32], yd[32];
+                ptx::tmem_ld32(sbuf, ya);
+                ptx::tmem_ld32(sbuf + 32, yb);
+                ptx::tmem_wait_ld();
+                ptx::tmem_ld32(sbuf + 64, yc);
+                ptx::tmem_ld32(sbuf + 96, yd);
+                scaled(ya, 0);
+                scaled(yb, 1);
+                float mx = fmaxf(top(ya), top(yb));
+                ptx::tmem_wait_ld();
+                ptx::tmem_ld32(sbuf, ya);
+                scaled(yc, 2);
+                scaled(yd, 3);
+                mx = ptx::max3(mx, top(yc), top(yd));
                 if constexpr (!kCodes) mx *= scale_log2;
                 const float m_new = fmaxf(m_run, mx);
                 const bool need = m_new > m_run + kRescaleLog2;
@@ -645,14 +689,13 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 const float base = m_use == -INFINITY ? 0.f : m_use;  // nothing seen yet: weights 2^-inf
                 const float2 nm = make_float2(-base, -base);
                 float2 sum4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-                uint32_t pk[64];
-                // P (bf16 pairs) over the first 64 columns of the S buffer, in
-                // two halves of 64 keys, each handed to the issuer when stored
+                // columns 32 c ... -> P, bf16 pairs in columns 64 + 16 c ... of the
+                // buffer (behind the scores that are still to be loaded again)
+                auto weigh = [&](const uint32_t(&y)[32], int c) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                    for (int i = 32 * hf; i < 32 * hf + 32; ++i) {
-                        const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 xi = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
                         float2 e;
                         if constexpr (kCodes)
                             e = ptx::add2(xi, nm);
@@ -664,37 +707,49 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                         sum4[i & 3] = ptx::add2(sum4[i & 3], p);
                         if constexpr (kCodes) {
                             // (a hidden value's scale may be anything)
-                            const float2 v2 = *reinterpret_cast<const float2*>(vscale + 2 * i);
+                            const float2 v2 = *reinterpret_cast<const float2*>(vscale + 32 * c + 2 * i);
                             float2 w = ptx::mul2(p, v2);
                             if (masked) {
-                                w.x = xi.x == -INFINITY ? 0.f : w.x;
-                                w.y = xi.y == -INFINITY ? 0.f : w.y;
+                                w.x = p.x == 0.f ? 0.f : w.x;
+                                w.y = p.y == 0.f ? 0.f : w.y;
                             }
                             pk[i] = ptx::pack_bf16x2(w.x, w.y);
                         } else {
                             pk[i] = ptx::pack_bf16x2(p.x, p.y);
                         }
                     }
-                    if (hf == 0 && j > j0 && __any_sync(0xffffffffu, need)) {
-                        // rescale O_w before this item's P V adds to it: S of
-                        // this item was committed after the P V of the previous
-                        // one, so that is done
+                    ptx::tmem_st16(sbuf + 64u + 16u * c, pk);
+                };
+                weigh(yc, 2);
+                weigh(yd, 3);
+                if (j > j0 && __any_sync(0xffffffffu, need)) {
+                    // rescale O_w before this item's P V adds to it: S of this
+                    // item was committed after the P V of the previous one, so
+                    // that is done
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[32];
-                            ptx::tmem_ld32(obuf + (uint32_t)c * 32, o);
-                            ptx::tmem_wait_ld();
-                            ptx::reg_fence(o);
+                    for (int b = 0; b < 8; ++b) {
+                        uint32_t o[16];
+                        ptx::tmem_ld16(obuf + (uint32_t)b * 16, o);
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence16(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-                            ptx::tmem_st32(obuf + (uint32_t)c * 32, o);
-                        }
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                        ptx::tmem_st16(obuf + (uint32_t)b * 16, o);
                     }
-                    ptx::tmem_st32_u(sbuf + 32u * hf, pk + 32 * hf);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    arrive1(hf == 0 ? &sm.p_half[wg] : &sm.p_full[wg]);
                 }
+                ptx::tmem_wait_ld();
+                ptx::tmem_ld32(sbuf + 32, yb);
+                scaled(ya, 0);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                arrive1(&sm.p_half[wg]);
+                weigh(ya, 0);
+                ptx::tmem_wait_ld();
+                scaled(yb, 1);
+                weigh(yb, 1);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                arrive1(&sm.p_full[wg]);
                 const float2 s2 = ptx::add2(ptx::add2(sum4[0], sum4[1]), ptx::add2(sum4[2], sum4[3]));
                 l_run = l_run * corr + (s2.x + s2.y);
                 m_run = m_use;
@@ -702,6 +757,13 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             if (!ok) break;
             blk += n;
             // ------------------------------------------------ epilogue --
+            // (the row's place again, from a number the compiler cannot see
+            // through: kept over the loop it would cost its registers)
+            int row_again = row;
+            asm volatile("" : "+r"(row_again));
+            const RowOf r = row_of(d, row_again, wg, g.G, HT);
+            const int token = r.token, head = r.head;
+            const bool valid = r.valid;
             const bool has[2] = {n > 0, pair ? n > 0 : n > 1};
             // the row's statistics over the piece, and what O_0 and O_1 count
             float m = m_run, l = l_run, f0 = 1.f, f1 = 1.f;
@@ -733,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                                  ((size_t)(d.row0 + token) * g.Hq + head) * kD;
-            const int slot = cut ? paged::partial_slot(pl, blockIdx.x, d.base) : 0;
+            const int slot = cut ? paged::partial_slot(sm.pl, blockIdx.x, d.base) : 0;
             const int half = pair ? wg : 0;
             float4* part = reinterpret_cast<float4*>(a.work.o) + (size_t)slot * 2 * 32 * kRows + half * 32 * kRows + row;
             float zero = 0.f;
@@ -817,14 +879,14 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             if (sm.last && valid) {
                 __threadfence();
                 const float2* ml = a.work.ml + half * kRows + row;
-                auto slot_of = [&](int c) { return (size_t)paged::partial_slot(pl, c, d.base); };
+                auto slot_of = [&](int c) { return (size_t)paged::partial_slot(sm.pl, c, d.base); };
                 float mm = -INFINITY, ll = 0.f;
                 for (int c = d.c0; c <= d.c1; ++c) mm = fmaxf(mm, __ldcg(ml + slot_of(c) * 2 * kRows).x);
                 for (int c = d.c0; c <= d.c1; ++c) {
                     const float2 x = __ldcg(ml + slot_of(c) * 2 * kRows);
                     ll += x.x == -INFINITY ? x.y : x.y * ptx::ex2(x.x - mm);
                 }
-                const float r = ll == 0.f ? 0.f : 1.f / ll;
+                const float inv_l = ll == 0.f ? 0.f : 1.f / ll;
                 const float4* po = reinterpret_cast<const float4*>(a.work.o) + (size_t)half * 32 * kRows +
                                    (size_t)(col0 / 4) * kRows + row;
 #pragma unroll 1
@@ -850,7 +912,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            w[e] = ptx::pack_bf16x2(acc[8 * i + 2 * e] * r, acc[8 * i + 2 * e + 1] * r);
+                            w[e] = ptx::pack_bf16x2(acc[8 * i + 2 * e] * inv_l, acc[8 * i + 2 * e + 1] * inv_l);
                         *reinterpret_cast<uint4*>(out + col0 + 32 * c8 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
