@@ -15,13 +15,20 @@
 // warpgroup's softmax runs beside the other's products.
 //
 // Roles: warp 0 loads (TMA: Q tiles, and each block's pages, found through
-// the page table, straight into one ring of K and V tiles), warp 1 issues the
-// products, warp 2 holds the TMEM, warp 3 clears the slots behind the last
-// key of a page (bf16 pages: what lies there may be NaN, and 0 x NaN is not
-// 0), warps 4-11 are the two softmax warpgroups and write the outputs.  With
-// codes warps 12-15 turn each staged block of codes into a bf16 tile: a code's
-// value is exact in bf16; the key's scale multiplies its scores, the value's
-// scale its weight, both in fp32.
+// the page table, into the rings of K and V tiles), warp 1 issues the products,
+// warp 2 holds the TMEM, warp 3 clears the slots behind the last key of a page
+// (bf16 pages: what lies there may be NaN, and 0 x NaN is not 0), warps 4-11
+// are the two softmax warpgroups and write the outputs.
+//
+// Pages of codes.  S takes K's codes as they are, with Q as the sum of two e4m3
+// terms: q 2^k = hi + lo, k per row so that the largest element lies in [2^7,
+// 2^8).  An element's 8 bits fit the two terms' 4 + 4 exactly down to 2^-2; below,
+// lo is a subnormal and off by at most 2^-10, 2^-17 of the row's largest
+// element.  e4m3 products run at twice the rate of bf16 ones, so two terms cost
+// what one bf16 product does, and K needs no conversion.  P has no such split
+// (its small weights would need bf16's exponents): V's codes become bf16 tiles,
+// exactly, in warps 12-15, which also split Q.  The keys' scales multiply their
+// scores and the values' scales the weights, in fp32.
 //
 // Softmax statistics, sums and accumulators are fp32.  The weights are
 // rounded to bf16, the type of the product with V; the sum they are divided
@@ -59,8 +66,10 @@ constexpr int kMinUnits = 2;
 template <bool kCodes>
 struct Cfg {
     static constexpr int kThreads = kCodes ? 512 : 384;
-    static constexpr int kStages = kCodes ? 3 : 4;  // K/V tiles in the ring
-    static constexpr int kStaged = kCodes ? 3 : 1;  // blocks of codes on their way
+    static constexpr int kK = kCodes ? 3 : 2;       // K tiles in their ring
+    static constexpr int kKBytes = kCodes ? kCodeTile : (int)kTileBytes;
+    static constexpr int kV = 2;                    // V tiles (bf16) in theirs
+    static constexpr int kStaged = 2;               // blocks of V's codes on their way
     // Registers per thread at launch (one CTA per SM) and after the split:
     // the other warpgroups hand theirs to the two softmax warpgroups.
     static constexpr int kRegsLaunch = kCodes ? 128 : 168;
@@ -87,18 +96,26 @@ struct Desc {
 
 template <bool kCodes>
 struct __align__(1024) Smem {
+    using C = Cfg<kCodes>;
     uint8_t q[2][kTileBytes];
-    uint8_t kv[Cfg<kCodes>::kStages][kTileBytes];
-    uint8_t st[kCodes ? Cfg<kCodes>::kStaged : 1][kCodes ? kCodeTile : 16];
-    // scratch of the plan, then four slots of a block's key scales (times the
-    // softmax scale, log2 units) and value scales
-    __align__(16) int scratch[kPagedMaxSeqs + 4];
-    __device__ float* ks(int slot) { return reinterpret_cast<float*>(scratch) + slot * kKB; }
-    __device__ float* vs(int slot) { return reinterpret_cast<float*>(scratch) + (4 + slot) * kKB; }
+    uint8_t k[C::kK][C::kKBytes];
+    uint8_t v[C::kV][kTileBytes];
+    uint8_t st[kCodes ? C::kStaged : 1][kCodes ? kCodeTile : 16];
+    // scratch of the plan, then (codes) the blocks' key and value scales: K of
+    // block j is loaded when S of block j - 3 is done, and with two warpgroups
+    // on alternate blocks the one before may still be in use
+    static constexpr int kScaleSlots = 5;
+    __align__(16) int scratch[kCodes ? kScaleSlots * 2 * kKB : kPagedMaxSeqs + 4];
+    static_assert(kScaleSlots * 2 * kKB > kPagedMaxSeqs, "scratch");
+    __device__ float* ks(int blk) { return reinterpret_cast<float*>(scratch) + blk % kScaleSlots * 2 * kKB; }
+    __device__ float* vs(int blk) { return ks(blk) + kKB; }
+    float ones[kCodes ? kKB : 4];
+    float row_scale[kCodes ? 4 : 1][kRows];  // 2^-k of Q's rows times the softmax scale (log2 units)
     uint64_t d_full[kDescs], d_empty[kDescs];
-    uint64_t q_full[2], q_empty[2];
-    uint64_t kv_full[4], kv_empty[4];
-    uint64_t st_full[4], st_empty[4];
+    uint64_t q_raw[2], q_full[2], q_empty[2];  // (q_raw: before the split in two terms)
+    uint64_t k_full[3], k_empty[3];
+    uint64_t v_full[2], v_empty[2];
+    uint64_t st_full[2], st_empty[2];
     uint64_t v_tail;             // a ragged block of V has landed, its tail not cleared yet
     uint64_t s_full[2];          // S of warpgroup w's item is in TMEM
     uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the last / first 64 keys written
@@ -106,8 +123,7 @@ struct __align__(1024) Smem {
     uint64_t o_free;             // 8 warp arrivals per piece: O_0, O_1 read out
     uint64_t ebar;               // 8 warp arrivals: the softmax warps meet
     uint64_t drain;
-    float ones[kCodes ? kKB : 4];
-    float red_m[2][2][kRows], red_l[2][2][kRows];  // [piece & 1][warpgroup][row]
+    float red_m[2][kRows], red_l[2][kRows];  // [warpgroup][row]
     Desc desc[kDescs];
     uint32_t tmem_base;
     int abort;
@@ -127,6 +143,49 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
     constexpr uint32_t k2p120 = 0x7b807b80u;  // 2^120 twice
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(k2p120));
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k2p120));
+}
+
+// The first `rows` rows of a Q tile (two swizzled halves of 64 features), in
+// place, into two tiles of e4m3 terms: row r of the halves lies where row r of
+// the terms goes.  16 lanes hold a row.  row_scale: 2^-k scale; NaN for a row
+// that is not finite.
+__device__ __forceinline__ void split_q(uint8_t* tile, float* row_scale, int rows, int cw, float scale) {
+    const int lane = threadIdx.x & 31, c = lane & 15;
+    for (int r0 = cw * 2; r0 < rows; r0 += 8) {
+        const int r = r0 + (lane >> 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(tile + ptx::tile_chunk_offset(r, c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        float x[8], amax = 0.f;
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+            amax = fmaxf(amax, fabsf(x[i]));
+            finite = finite && fabsf(x[i]) < INFINITY;
+        }
+        if (!finite) amax = INFINITY;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // (every lane has read the row: it may be overwritten)
+        int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);  // amax 2^k in [2^7, 2^8)
+        k = k > 120 ? 120 : k;
+        const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
+        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float2 y = make_float2(x[i] * up, x[i + 1] * up);
+            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+            const __nv_fp8x2_storage_t l =
+                __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+            hi[i >> 2] |= (uint32_t)h << (8 * (i & 2));
+            lo[i >> 2] |= (uint32_t)l << (8 * (i & 2));
+        }
+        uint8_t* to = tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(to + kHalfBytes) = make_uint2(lo[0], lo[1]);
+        if (c == 0) row_scale[r] = amax < INFINITY ? down * scale : __int_as_float(0x7fffffff);
+    }
 }
 
 __device__ __forceinline__ uint32_t bits_below(int n) {
@@ -185,9 +244,13 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttend a,
                     float scale_log2) {
     using C = Cfg<kCodes>;
-    extern __shared__ uint8_t smem_raw[];
-    Smem<kCodes>& sm = *reinterpret_cast<Smem<kCodes>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                        ~static_cast<uintptr_t>(1023));
+    // (the swizzled tiles need 1024-byte boundaries; there is no room to align by hand)
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem<kCodes>& sm = *reinterpret_cast<Smem<kCodes>*>(smem_raw);
+    if (ptx::smem_u32(smem_raw) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(a.err, kErrPagedTimeout);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PagedGeom& g = a.g;
     volatile int* abort = &sm.abort;
@@ -198,14 +261,17 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             init(&sm.d_full[i], 1);
             init(&sm.d_empty[i], 1 + kSoftmaxWarps + (kCodes ? kConvWarps : 1));
         }
-        for (int i = 0; i < 4; ++i) {
-            init(&sm.kv_full[i], kCodes ? kConvWarps : 1);
-            init(&sm.kv_empty[i], 1);
-            init(&sm.st_full[i], 1);
-            init(&sm.st_empty[i], kConvWarps);
+        for (int i = 0; i < 3; ++i) {
+            init(&sm.k_full[i], 1);
+            init(&sm.k_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            init(&sm.q_full[i], 1);
+            init(&sm.v_full[i], kCodes ? kConvWarps : 1);
+            init(&sm.v_empty[i], 1);
+            init(&sm.st_full[i], 1);
+            init(&sm.st_empty[i], kConvWarps);
+            init(&sm.q_raw[i], 1);
+            init(&sm.q_full[i], kCodes ? kConvWarps : 1);
             init(&sm.q_empty[i], 1);
             init(&sm.s_full[i], 1);
             init(&sm.p_half[i], kWgWarps);
@@ -261,9 +327,11 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
         paged::Cursor cur = pl.first;
         const int page_tokens = 1 << g.page_log2;
-        const int per_block = page_tokens < kKB ? kKB >> g.page_log2 : 1;  // pages of a block
+        const int pb_log2 = page_tokens < kKB ? 7 - g.page_log2 : 0;      // pages of a block
+        const int per_block = 1 << pb_log2;
         const int absent = g.pages * g.Hk;                                // reads as zeros
-        int cnt = 0, qn = 0, tails = 0;
+        const int batch_log2 = 5 - pb_log2;  // blocks whose pages 32 lanes look up at once
+        int kn = 0, vn = 0, qn = 0, tails = 0;
         bool ok = true, more = pl.u1 > pl.u0;
         for (int si = 0; ok; ++si) {
             const int slot = si % kDescs;
@@ -292,7 +360,8 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = ptx::smem_u32(&sm.q_full[qs]), dst = ptx::smem_u32(sm.q[qs]);
+                    const uint32_t bar = ptx::smem_u32(kCodes ? &sm.q_raw[qs] : &sm.q_full[qs]);
+                    const uint32_t dst = ptx::smem_u32(sm.q[qs]);
                     ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(HT * g.G) * 256u);
                     const int row = pc.q.q0 + pc.i0 + t * HT;
                     ptx::tma_load_4d_w(dst, &tm_q, 0, cur.h * g.G, row, 0, bar);
@@ -301,87 +370,110 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 // keys that some query of the tile sees: [0, see_sink) and [see_lo, see_end)
                 const paged::Sight last = paged::sight(a.mask, at0 + pc.n - 1, pc.q.total);
                 const int see_lo = paged::sight(a.mask, at0 < 0 ? 0 : at0, pc.q.total).lo;
-                // this lane's page of piece block j: its place in the pool, or absent
-                auto look_up = [&](int j) -> int {
-                    if (j >= n || lane >= per_block) return absent;
-                    const int k0 = pc.blocks.at(pc.b0 + j) * kKB + (lane << g.page_log2);
-                    const int span = page_tokens < kKB ? page_tokens : kKB;
-                    if (k0 >= last.end || (k0 + span <= see_lo && k0 >= last.sink)) return absent;
-                    const int p = a.seqs.table[(size_t)cur.s * a.seqs.max_pages + (k0 >> g.page_log2)];
-                    if ((unsigned)p < (unsigned)g.pages) return p * g.Hk + cur.h;
+                // Places in the pool (page x heads + head, or absent) of a batch of
+                // blocks, one page per lane; a batch is looked up two batches
+                // before it is needed, so nobody waits for the page table.
+                const int span = page_tokens < kKB ? page_tokens : kKB;
+                auto look_up = [&](int b, uint32_t& needed) -> int {
+                    const int j = (b << batch_log2) + (lane >> pb_log2);
+                    const int k0 = pc.blocks.at(pc.b0 + j) * kKB + ((lane & (per_block - 1)) << g.page_log2);
+                    const bool need = j < n && k0 < last.end && (k0 + span > see_lo || k0 < last.sink);
+                    needed = __ballot_sync(0xffffffffu, need);
+                    return need ? a.seqs.table[(size_t)cur.s * a.seqs.max_pages + (k0 >> g.page_log2)] : 0;
+                };
+                uint32_t n0, n1, n2;
+                int b0 = look_up(0, n0), b1 = look_up(1, n1), b2 = look_up(2, n2), b_at = 0;
+                // this lane's place of block j, in batch b_at or the next one
+                auto place_of = [&](int j) -> int {
+                    const bool later = (j >> batch_log2) > b_at;
+                    const int src = ((j << pb_log2) & 31) + (lane & (per_block - 1));
+                    const int page = __shfl_sync(0xffffffffu, later ? b1 : b0, src);
+                    if (lane >= per_block || !(((later ? n1 : n0) >> src) & 1u)) return absent;
+                    if ((unsigned)page < (unsigned)g.pages) return page * g.Hk + cur.h;
                     paged::report(a.err, kErrPagedTable);
                     return absent;
                 };
-                auto load = [&](int j, int place, const CUtensorMap* tm, bool is_v) -> bool {
-                    const int key0 = pc.blocks.at(pc.b0 + j) * kKB;
-                    const int slot0 = key0 & (page_tokens - 1);
-                    if constexpr (kCodes) {
-                        const int s = cnt % C::kStaged;
-                        if (cnt >= C::kStaged && !wwait(&sm.st_empty[s], (cnt / C::kStaged - 1) & 1)) return false;
-                        const uint32_t bar = ptx::smem_u32(&sm.st_full[s]);
-                        ptx::mbar_arrive_expect_tx_w(bar, kCodeTile);
-                        __syncwarp();
-                        if (lane < per_block)
-                            ptx::tma_load_4d(ptx::smem_u32(sm.st[s]) + (uint32_t)(lane << g.page_log2) * 128u, tm, 0,
-                                             slot0, place, 0, bar);
-                    } else {
-                        const int s = cnt % C::kStages;
-                        if (cnt >= C::kStages && !wwait(&sm.kv_empty[s], (cnt / C::kStages - 1) & 1)) return false;
-                        uint64_t* full = &sm.kv_full[s];
-                        if (is_v && j == n - 1 && key0 + kKB > pc.q.total) {
-                            full = &sm.v_tail;  // (the previous use has been waited for by warp 3)
-                            ++tails;
-                        }
-                        const uint32_t bar = ptx::smem_u32(full);
-                        ptx::mbar_arrive_expect_tx_w(bar, kTileBytes);
-                        __syncwarp();
-                        if (lane < per_block) {
-                            const uint32_t dst = ptx::smem_u32(sm.kv[s]) + (uint32_t)(lane << g.page_log2) * 128u;
-                            ptx::tma_load_4d(dst, tm, 0, slot0, place, 0, bar);
-                            ptx::tma_load_4d(dst + kHalfBytes, tm, 64, slot0, place, 0, bar);
+                auto load_k = [&](int j) -> bool {
+                    const int s = kn % C::kK;
+                    if (kn >= C::kK && !wwait(&sm.k_empty[s], (kn / C::kK - 1) & 1)) return false;
+                    const int place = place_of(j);
+                    const int slot0 = pc.blocks.at(pc.b0 + j) * kKB & (page_tokens - 1);
+                    const uint32_t bar = ptx::smem_u32(&sm.k_full[s]);
+                    const uint32_t there = __popc(__ballot_sync(0xffffffffu, place != absent));
+                    ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)C::kKBytes + (kCodes ? there * (uint32_t)span * 8u : 0u));
+                    __syncwarp();
+                    if (lane < per_block) {
+                        const uint32_t at = (uint32_t)(lane << g.page_log2);  // first row of the page in the tile
+                        const uint32_t dst = ptx::smem_u32(sm.k[s]) + at * 128u;
+                        ptx::tma_load_4d(dst, &tm_k, 0, slot0, place, 0, bar);
+                        if constexpr (kCodes) {
+                            if (place != absent) {
+                                const size_t row = ((size_t)place << g.page_log2) + slot0;
+                                ptx::bulk_load(ptx::smem_u32(sm.ks(kn) + at), a.pool.ks + row, span * 4u, bar);
+                                ptx::bulk_load(ptx::smem_u32(sm.vs(kn) + at), a.pool.vs + row, span * 4u, bar);
+                            }
+                        } else {
+                            ptx::tma_load_4d(dst + kHalfBytes, &tm_k, 64, slot0, place, 0, bar);
                         }
                     }
                     __syncwarp();
-                    ++cnt;
+                    ++kn;
                     return true;
                 };
-                // K runs one item ahead of V for each warpgroup: the order in
-                // which the products take them
-                int p0 = look_up(0), p1 = look_up(1), p2 = look_up(2);
-                if (ok) ok = load(0, p0, &tm_k, false);
-                if (ok && !pair && n > 1) ok = load(1, p1, &tm_k, false);
+                auto load_v = [&](int j) -> bool {
+                    const int s = vn & 1;
+                    if (vn >= 2 && !wwait(kCodes ? &sm.st_empty[s] : &sm.v_empty[s], ((vn >> 1) - 1) & 1)) return false;
+                    const int place = place_of(j);
+                    const int key0 = pc.blocks.at(pc.b0 + j) * kKB;
+                    const int slot0 = key0 & (page_tokens - 1);
+                    uint64_t* full = kCodes ? &sm.st_full[s] : &sm.v_full[s];
+                    if (!kCodes && j == n - 1 && key0 + kKB > pc.q.total) {
+                        full = &sm.v_tail;  // warp 3 clears the tail and hands it on
+                        ++tails;
+                    }
+                    const uint32_t bar = ptx::smem_u32(full);
+                    ptx::mbar_arrive_expect_tx_w(bar, kCodes ? kCodeTile : kTileBytes);
+                    __syncwarp();
+                    if (lane < per_block) {
+                        const uint32_t dst = (kCodes ? ptx::smem_u32(sm.st[s]) : ptx::smem_u32(sm.v[s])) +
+                                             (uint32_t)(lane << g.page_log2) * 128u;
+                        ptx::tma_load_4d(dst, &tm_v, 0, slot0, place, 0, bar);
+                        if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_v, 64, slot0, place, 0, bar);
+                    }
+                    __syncwarp();
+                    ++vn;
+                    return true;
+                };
+                // in the order in which the products take them; the K ring
+                // may be that much ahead
+                for (int j = 0; ok && j < C::kK && j < n; ++j) ok = load_k(j);
                 for (int j = 0; ok && j < n; ++j) {
-                    const int p3 = look_up(j + 3);
-                    ok = load(j, p0, &tm_v, true);
-                    const int next = j + (pair ? 1 : 2);
-                    if (ok && next < n) ok = load(next, pair ? p1 : p2, &tm_k, false);
-                    p0 = p1;
-                    p1 = p2;
-                    p2 = p3;
+                    ok = load_v(j);
+                    if (ok && j + C::kK < n) ok = load_k(j + C::kK);
+                    if (((j + 1) & ((1 << batch_log2) - 1)) == 0) {
+                        b0 = b1, n0 = n1;
+                        b1 = b2, n1 = n2;
+                        ++b_at;
+                        b2 = look_up(b_at + 2, n2);
+                    }
                 }
             }
             more = paged::advance(sm.plan, pl, a.seqs, TQ, pc.units, cur);
         }
         if (!ok) fail();
         // the last loads of each ring have landed before exit
-        if constexpr (kCodes) {
-            for (int i = cnt > C::kStaged ? cnt - C::kStaged : 0; i < cnt; ++i)
-                ptx::mbar_wait_bounded(ptx::smem_u32(&sm.st_full[i % C::kStaged]), (i / C::kStaged) & 1, &no_abort,
-                                       kWaitLimitNs);
-        } else {
-            if (tails)
-                ptx::mbar_wait_bounded(ptx::smem_u32(&sm.v_tail), (tails - 1) & 1, &no_abort, kWaitLimitNs);
-            for (int i = cnt > C::kStages ? cnt - C::kStages : 0; i < cnt; ++i)
-                ptx::mbar_wait_bounded(ptx::smem_u32(&sm.kv_full[i % C::kStages]), (i / C::kStages) & 1, &no_abort,
-                                       kWaitLimitNs);
-        }
-        for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i)
-            ptx::mbar_wait_bounded(ptx::smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, &no_abort, kWaitLimitNs);
+        auto landed = [&](uint64_t* bar, int use) {
+            ptx::mbar_wait_bounded(ptx::smem_u32(bar), use & 1, &no_abort, kWaitLimitNs);
+        };
+        for (int i = kn > C::kK ? kn - C::kK : 0; i < kn; ++i) landed(&sm.k_full[i % C::kK], i / C::kK);
+        if (tails) landed(&sm.v_tail, tails - 1);
+        for (int i = vn > 2 ? vn - 2 : 0; i < vn; ++i) landed(kCodes ? &sm.st_full[i & 1] : &sm.v_full[i & 1], i >> 1);
+        for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i) landed(kCodes ? &sm.q_raw[i & 1] : &sm.q_full[i & 1], i >> 1);
     } else if (warp == 1) {
         // ------------------------------------------------------ issuer --
-        const uint32_t idesc_s = ptx::idesc_bf16_f32(kRows, kKB, false, false);
+        const uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(kRows, kKB) : ptx::idesc_bf16_f32(kRows, kKB, false, false);
         const uint32_t idesc_pv = ptx::idesc_bf16_f32(kRows, kD, false, true);  // V: MN-major
-        int cnt = 0, qn = 0, pieces = 0;
+        int kn = 0, vn = 0, qn = 0, pieces = 0;
         uint32_t p_par = 0;
         bool ok = true;
         for (int si = 0; ok; ++si) {
@@ -397,24 +489,24 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             const int N = pair ? 2 * n : n;
             const int q0 = qn, nq = pair ? 2 : 1;
             for (int t = 0; ok && t < nq; ++t, ++qn) ok = wwait(&sm.q_full[qn & 1], (qn >> 1) & 1);
-            int ks = 0, vs = 0;  // ring stages of the K and V tile in use
-            // the ring's next tile, in the order it was loaded
-            auto take = [&](int& s) -> bool {
-                s = cnt % C::kStages;
-                if (!wwait(&sm.kv_full[s], (cnt / C::kStages) & 1)) return false;
-                ++cnt;
-                return true;
+            int ks = 0, vs = 0;       // ring stages of the K and V tile in use
+            const bool keep = pair;   // a tile serves two items
+            auto s_ready = [&](int i) -> bool {
+                if (keep && (i & 1)) return true;
+                ks = kn % C::kK;
+                return wwait(&sm.k_full[ks], (kn++ / C::kK) & 1);
             };
-            const bool keep = pair;  // a tile serves two items
-            auto s_ready = [&](int i) -> bool { return (keep && (i & 1)) || take(ks); };
             auto s_issue = [&](int i) {
                 ptx::tc_fence_after();
                 const uint32_t q_s = ptx::smem_u32(sm.q[(q0 + (pair ? i & 1 : 0)) & 1]);
-                const uint32_t k_s = ptx::smem_u32(sm.kv[ks]);
-                ptx::umma_ss8_kk(tmem + kColS + (uint32_t)(i & 1) * kKB, ptx::kmajor_desc(q_s, 0),
-                                 ptx::kmajor_desc(k_s, 0), idesc_s, 0u);
+                const uint32_t k_s = ptx::smem_u32(sm.k[ks]);
+                const uint32_t s_t = tmem + kColS + (uint32_t)(i & 1) * kKB;
+                if constexpr (kCodes)
+                    ptx::umma_e4m3_two_terms(s_t, ptx::kmajor_desc(q_s, 0), ptx::kmajor_desc(k_s, 0), idesc_s);
+                else
+                    ptx::umma_ss8_kk(s_t, ptx::kmajor_desc(q_s, 0), ptx::kmajor_desc(k_s, 0), idesc_s, 0u);
                 ptx::umma_commit_w(ptx::smem_u32(&sm.s_full[i & 1]));
-                if (!keep || (i & 1)) ptx::umma_commit_w(ptx::smem_u32(&sm.kv_empty[ks]));
+                if (!keep || (i & 1)) ptx::umma_commit_w(ptx::smem_u32(&sm.k_empty[ks]));
                 if (i == N - 1)
                     for (int t = 0; t < nq; ++t) ptx::umma_commit_w(ptx::smem_u32(&sm.q_empty[(q0 + t) & 1]));
             };
@@ -429,13 +521,16 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 const int w = i & 1;
                 const uint32_t par = (p_par >> w) & 1;
                 p_par ^= 1u << w;
-                if (!keep || w == 0) ok = take(vs);
+                if (!keep || w == 0) {
+                    vs = vn & 1;
+                    ok = wwait(&sm.v_full[vs], (vn++ >> 1) & 1);
+                }
                 ok = ok && wwait(&sm.p_half[w], par);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t p_t = tmem + kColS + (uint32_t)w * kKB + 64u;
                 const uint32_t o_t = tmem + kColO + (uint32_t)w * kD;
-                const uint32_t v_s = ptx::smem_u32(sm.kv[vs]);
+                const uint32_t v_s = ptx::smem_u32(sm.v[vs]);
                 // O_w += P V in two halves of 64 keys, the last 64 first: they
                 // run while the softmax warps work on the other half's P
                 ptx::umma_ts4_mn(o_t, p_t + 32u, ptx::mnmajor_desc(v_s, 4), idesc_pv, i >= 2 ? 1u : 0u);
@@ -444,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 if (!ok) break;
                 ptx::tc_fence_after();
                 ptx::umma_ts4_mn(o_t, p_t, ptx::mnmajor_desc(v_s, 0), idesc_pv, 1u);
-                if (!keep || w == 1) ptx::umma_commit_w(ptx::smem_u32(&sm.kv_empty[vs]));
+                if (!keep || w == 1) ptx::umma_commit_w(ptx::smem_u32(&sm.v_empty[vs]));
                 if (next)
                     s_issue(i + 2);
                 else
@@ -460,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
     } else if (warp == 3) {
         // ----------------------------------- slots behind the last key --
         if constexpr (!kCodes) {
-            int cnt = 0, tails = 0;
+            int vn = 0, tails = 0;
             bool ok = true;
             for (int si = 0; ok; ++si) {
                 Desc d;
@@ -471,28 +566,28 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 if (d.done) break;
                 const int n = d.b1 - d.b0;
                 if (n <= 0) continue;
-                cnt += 2 * n;
+                vn += n;
                 const int key0 = d.key0(n - 1);
                 if (key0 + kKB <= d.total) continue;
                 ok = wwait(&sm.v_tail, tails & 1);
                 ++tails;
                 if (!ok) break;
-                const int s = (cnt - 1) % C::kStages;  // the piece's last tile
+                const int s = (vn - 1) & 1;  // the piece's last tile
                 const int first = d.total > key0 ? d.total - key0 : 0;
                 for (int half = 0; half < 2; ++half)
                     for (int at = first * 128 + lane * 16; at < (int)kHalfBytes; at += 512)
-                        *reinterpret_cast<uint4*>(sm.kv[s] + half * kHalfBytes + at) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(sm.v[s] + half * kHalfBytes + at) = make_uint4(0u, 0u, 0u, 0u);
                 ptx::fence_proxy_async_smem();
-                arrive1(&sm.kv_full[s]);
+                arrive1(&sm.v_full[s]);
             }
             if (!ok) fail();
         }
     } else if (warp >= 12) {
-        // --------------------------------------- codes -> bf16 tiles --
+        // ----------------- Q in two terms, V's codes -> bf16 tiles --
         if constexpr (kCodes) {
             ptx::setmaxnreg_dec<C::kRegsConv>();
-            const int cw = warp - 12, tid = threadIdx.x - 384;  // tid: a key of the block
-            int cnt = 0, blk = 0;
+            const int cw = warp - 12;
+            int vn = 0, qn = 0;
             bool ok = true;
             for (int si = 0; ok; ++si) {
                 Desc d;
@@ -503,65 +598,42 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 if (d.done) break;
                 const int n = d.b1 - d.b0;
                 if (n <= 0) continue;
-                const bool pair = d.pair != 0;
-                const int end = paged::sight(a.mask, d.at0 + d.n - 1, d.total).end;
-                auto scales = [&](int j) -> float2 {  // of this thread's key of piece block j
-                    if (j >= n) return make_float2(0.f, 0.f);
-                    const int key = d.key0(j) + tid;
-                    if (key >= end) return make_float2(0.f, 0.f);
-                    const int p = a.seqs.table[(size_t)d.s * a.seqs.max_pages + (key >> g.page_log2)];
-                    if ((unsigned)p >= (unsigned)g.pages) return make_float2(0.f, 0.f);  // (reported by the loader)
-                    const size_t row = paged::pool_row(g, p, d.h, key);
-                    return make_float2(a.pool.ks[row], a.pool.vs[row]);
-                };
-                auto convert = [&](int j, bool is_k, float2 sc) -> bool {
-                    const int f = cnt % C::kStaged, s = cnt % C::kStages;
-                    if (!wwait(&sm.st_full[f], (cnt / C::kStaged) & 1)) return false;
-                    if (cnt >= C::kStages && !wwait(&sm.kv_empty[s], (cnt / C::kStages - 1) & 1)) return false;
-                    if (is_k) {  // (K waits for the V of three tiles before: the slot's readers are done)
-                        sm.ks((blk + j) & 3)[tid] = sc.x * scale_log2;
-                        sm.vs((blk + j) & 3)[tid] = sc.y;
-                    }
-                    const uint8_t* from = sm.st[f];
-                    const uint32_t to = ptx::smem_u32(sm.kv[s]);
-                    const int c = lane & 7;  // this lane's 16 features
-#pragma unroll 4
+                for (int t = 0; ok && t < (d.pair ? 2 : 1); ++t, ++qn) {
+                    const int qs = qn & 1;
+                    ok = wwait(&sm.q_raw[qs], (qn >> 1) & 1);
+                    if (!ok) break;
+                    const int tokens = d.n - t * HT < HT ? d.n - t * HT : HT;
+                    split_q(sm.q[qs], sm.row_scale[qn & 3], tokens * g.G, cw, scale_log2);
+                    ptx::fence_proxy_async_smem();
+                    arrive1(&sm.q_full[qs]);
+                }
+                for (int j = 0; ok && j < n; ++j, ++vn) {
+                    const int s = vn & 1;
+                    ok = wwait(&sm.st_full[s], (vn >> 1) & 1) && (vn < 2 || wwait(&sm.v_empty[s], ((vn >> 1) - 1) & 1));
+                    if (!ok) break;
+                    // lanes of a quarter warp take eight rows: loads and stores
+                    // of the swizzled tiles then touch every bank once
+                    const int r7 = lane & 7, c = lane >> 3;
+                    const uint8_t* from = sm.st[s] + (cw * 32 + r7) * 128 + ((c ^ r7) << 4);
+                    const uint32_t to = ptx::smem_u32(sm.v[s]) + (uint32_t)((cw * 32 + r7) * 128 + (((2 * c) ^ r7) << 4));
+                    const uint32_t to2 = to ^ 16u;
+                    const uint8_t* from2 = sm.st[s] + (cw * 32 + r7) * 128 + (((c + 4) ^ r7) << 4);
+#pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int r = cw * 32 + i * 4 + (lane >> 3);
-                        const uint4 u = *reinterpret_cast<const uint4*>(from + r * 128 + c * 16);
+                        const int half = i & 1, row8 = (i >> 1) * 1024;  // 16 codes: features 64 half + 16 c ..., 8 rows on
+                        const uint4 u = *reinterpret_cast<const uint4*>((half ? from2 : from) + row8);
                         uint32_t y[8];
                         codes_to_bf16(u.x, y[0], y[1]);
                         codes_to_bf16(u.y, y[2], y[3]);
                         codes_to_bf16(u.z, y[4], y[5]);
                         codes_to_bf16(u.w, y[6], y[7]);
-                        // (the lanes of the second half swap their two stores:
-                        // eight lanes then cover all banks)
-                        const bool sw = c >= 4;
-                        const int c0 = 2 * c + (sw ? 1 : 0), c1 = 2 * c + (sw ? 0 : 1);
-                        ptx::st_shared_v4(to + ptx::tile_chunk_offset(r, c0), sw ? y[4] : y[0], sw ? y[5] : y[1],
-                                          sw ? y[6] : y[2], sw ? y[7] : y[3]);
-                        ptx::st_shared_v4(to + ptx::tile_chunk_offset(r, c1), sw ? y[0] : y[4], sw ? y[1] : y[5],
-                                          sw ? y[2] : y[6], sw ? y[3] : y[7]);
+                        ptx::st_shared_v4(to + half * kHalfBytes + row8, y[0], y[1], y[2], y[3]);
+                        ptx::st_shared_v4(to2 + half * kHalfBytes + row8, y[4], y[5], y[6], y[7]);
                     }
                     ptx::fence_proxy_async_smem();
-                    arrive1(&sm.kv_full[s]);
-                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.st_empty[f]));
-                    ++cnt;
-                    return true;
-                };
-                const float2 s0 = scales(0);
-                float2 s1 = scales(1), s2 = scales(2);
-                ok = convert(0, true, s0);
-                if (ok && !pair && n > 1) ok = convert(1, true, s1);
-                for (int j = 0; ok && j < n; ++j) {
-                    const float2 s3 = scales(j + 3);
-                    ok = convert(j, false, s3);
-                    const int next = j + (pair ? 1 : 2);
-                    if (ok && next < n) ok = convert(next, true, pair ? s1 : s2);
-                    s1 = s2;
-                    s2 = s3;
+                    arrive1(&sm.v_full[s]);
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.st_empty[s]));
                 }
-                blk += n;
             }
             if (!ok) fail();
         }
@@ -581,7 +653,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             arrive1(&sm.ebar);
             return wwait(&sm.ebar, (e_uses++) & 1);
         };
-        const float2 sl2 = make_float2(scale_log2, scale_log2);
+        int qn = 0;
         for (int si = 0; ok; ++si) {
             // (read where it is, and given back at the piece's end: registers are short)
             ok = wwait(&sm.d_full[si % kDescs], (si / kDescs) & 1);
@@ -599,6 +671,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 busy = __any_sync(0xffffffffu, r.valid);
             }
             float m_run = -INFINITY, l_run = 0.f;
+            float row_mul = scale_log2;  // scores -> log2 units (codes: with the row's own factor)
             const int step = pair ? 1 : 2, j0 = pair ? 0 : wg;
             for (int j = j0; j < n; j += step) {
                 ok = wwait(&sm.s_full[wg], s_par);
@@ -611,6 +684,9 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const int key0 = d.key0(j);
+                const float* kscale = sm.ks(blk + j);
+                const float* vscale = kscale + kKB;
+                if (kCodes && j == j0) row_mul = sm.row_scale[(qn + (pair ? wg : 0)) & 3][row];
                 // nothing of the block is hidden from this row
                 const bool open = key0 + kKB <= see.end && (key0 >= see.lo || key0 + kKB <= see.sink);
                 const bool masked = __any_sync(0xffffffffu, !open);
@@ -630,15 +706,14 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                         for (int i = 0; i < 32; ++i) {
                             // (after the key's scale, which may be anything where the key is hidden)
                             if constexpr (kCodes)
-                                y[i] = __float_as_uint(__uint_as_float(y[i]) * sm.ks((blk + j) & 3)[32 * c + i]);
+                                y[i] = __float_as_uint(__uint_as_float(y[i]) * kscale[32 * c + i]);
                             y[i] = (seen >> i) & 1u ? y[i] : 0xff800000u;
                         }
                         ptx::tmem_st32(sbuf + (uint32_t)c * 32, y);
                     }
                     ptx::tmem_wait_st();
                 }
-                const float* kscale = kCodes && masked ? sm.ones : sm.ks((blk + j) & 3);
-                const float* vscale = sm.vs((blk + j) & 3);
+                if (kCodes && masked) kscale = sm.ones;  // (they are scaled already)
                 // columns 32 c .. 32 c + 31 of the scores (codes: times the key scales)
                 auto scaled = [&](uint32_t(&y)[32], int c) {
                     ptx::reg_fence(y);
@@ -681,7 +756,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 scaled(yc, 2);
                 scaled(yd, 3);
                 mx = ptx::max3(mx, top(yc), top(yd));
-                if constexpr (!kCodes) mx *= scale_log2;
+                mx *= row_mul;
                 const float m_new = fmaxf(m_run, mx);
                 const bool need = m_new > m_run + kRescaleLog2;
                 const float m_use = need ? m_new : m_run;
@@ -696,11 +771,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 xi = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
-                        float2 e;
-                        if constexpr (kCodes)
-                            e = ptx::add2(xi, nm);
-                        else
-                            e = ptx::fma2(xi, sl2, nm);
+                        const float2 e = ptx::fma2(xi, make_float2(row_mul, row_mul), nm);
                         float2 p;
                         p.x = ptx::ex2(e.x);
                         p.y = ptx::ex2(e.y);
@@ -756,6 +827,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             }
             if (!ok) break;
             blk += n;
+            if (n > 0) qn += pair ? 2 : 1;
             // ------------------------------------------------ epilogue --
             // (the row's place again, from a number the compiler cannot see
             // through: kept over the loop it would cost its registers)
@@ -768,18 +840,18 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             // the row's statistics over the piece, and what O_0 and O_1 count
             float m = m_run, l = l_run, f0 = 1.f, f1 = 1.f;
             if (!pair) {
-                float(&rm)[2][kRows] = sm.red_m[si & 1];
-                float(&rl)[2][kRows] = sm.red_l[si & 1];
-                rm[wg][row] = m_run;
-                rl[wg][row] = l_run;
+                sm.red_m[wg][row] = m_run;
+                sm.red_l[wg][row] = l_run;
                 ok = meet();
                 if (!ok) break;
-                const float m0 = rm[0][row], m1 = rm[1][row];
+                const float m0 = sm.red_m[0][row], m1 = sm.red_m[1][row];
                 m = fmaxf(m0, m1);
                 // (weights without a maximum are NaN or none)
                 f0 = m0 == -INFINITY ? 1.f : ptx::ex2(m0 - m);
                 f1 = m1 == -INFINITY ? 1.f : ptx::ex2(m1 - m);
-                l = f0 * rl[0][row] + f1 * rl[1][row];
+                l = f0 * sm.red_l[0][row] + f1 * sm.red_l[1][row];
+                ok = meet();  // (all have read: the next piece may write)
+                if (!ok) break;
             }
             for (int w = 0; ok && w < 2; ++w) {
                 if (!has[w]) continue;
@@ -933,8 +1005,8 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
 template <bool kCodes>
 bool ready() {
     const auto kernel = paged_tc_kernel<kCodes>;
-    static_assert(sizeof(Smem<kCodes>) + 1024 <= 232448, "shared memory");
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<kCodes>) + 1024) !=
+    static_assert(sizeof(Smem<kCodes>) <= 232448, "shared memory");
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<kCodes>)) !=
         cudaSuccess) {
         cudaGetLastError();
         return false;
@@ -964,7 +1036,7 @@ cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int grid = max_ctas > 0 && max_ctas < sms ? max_ctas : sms;
     static_assert(2 * 2 * kRows <= kPagedRowsPerSm, "workspace rows");
-    paged_tc_kernel<kCodes><<<grid, Cfg<kCodes>::kThreads, sizeof(Smem<kCodes>) + 1024, st>>>(
+    paged_tc_kernel<kCodes><<<grid, Cfg<kCodes>::kThreads, sizeof(Smem<kCodes>), st>>>(
         q, k, v, a, a.scale * 1.4426950408889634f);
     return cudaGetLastError();
 }

@@ -102,6 +102,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16; both ends on 16 bytes) into this
+// CTA's shared memory, completing tx bytes on bar.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 // 4-D tiled store from this CTA's shared memory (bulk async-group).  Rows
 // outside the tensor are not written.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, uint32_t src, int c0, int c1,
@@ -461,6 +470,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
            | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4)                      // D format fp32 (A and B formats 0: e4m3)
+           | ((uint32_t)(N >> 3) << 17)   // N / 8
+           | ((uint32_t)(M >> 4) << 24);  // M / 16
+}
+
 // Operand tiles of 128 rows x 128 bf16, stored as two 128-row x 64-column
 // halves of 16 KB with the 128-byte swizzle (the layout TMA writes for a
 // {64, ..., 128} box).
@@ -514,6 +530,36 @@ __device__ __forceinline__ void umma_ss8_kk(uint32_t d_tmem, uint64_t a0, uint64
         "add.u32 x, %1, 1030;\n\tadd.u32 y, %3, 1030;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, one;\n\t}" ::"r"(d_tmem),
         "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc0)
+        : "memory");
+}
+// D = A_0 B + A_1 B with e4m3 operands, 128 deep (four k-steps of 32 bytes
+// each): A_0 and A_1 are two K-major tiles of 128 rows x 128 bytes, 16 KB
+// apart, B one such tile.
+__device__ __forceinline__ void umma_e4m3_two_terms(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc) {
+    const uint32_t alo = (uint32_t)a0, ahi = (uint32_t)(a0 >> 32);
+    const uint32_t blo = (uint32_t)b0, bhi = (uint32_t)(b0 >> 32);
+    asm volatile(
+        "{\n\t.reg .pred e, p, one;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %5, %5;\n\t"
+        "setp.eq.b32 one, %5, %5;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
+        "add.u32 x, %1, 1024;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
+        "add.u32 x, %1, 1026;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
+        "add.u32 x, %1, 1028;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
+        "add.u32 x, %1, 1030;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t}" ::"r"(d_tmem),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc)
         : "memory");
 }
 // A from TMEM (a_tmem, 8 columns of bf16 pairs per k-step), B MN-major:

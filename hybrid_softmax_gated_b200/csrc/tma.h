@@ -33,9 +33,8 @@ bool tma_encode_rows_2d(CUtensorMap* m, const void* p, long long inner, long lon
 bool tma_encode_tiles(CUtensorMap* m, const void* p, int outer);
 
 // A pool of pages [outer][page][128] (outer = pages x heads), bf16 or (codes)
-// 8-bit: dims {128, page, outer, 1}; box {64, box_rows, 1, 1} with the
-// 128-byte swizzle, or for codes {128, box_rows, 1, 1} without one.  An outer
-// coordinate past the end reads as zeros.
+// 8-bit: dims {128, page, outer, 1}; box {64, box_rows, 1, 1}, for codes {128,
+// box_rows, 1, 1}.  An outer coordinate past the end reads as zeros.
 bool tma_encode_pages(CUtensorMap* m, const void* p, bool codes, int page, long long outer, int box_rows);
 
 // Tokens of a [tokens][heads][128] bf16 tensor, `stride` elements apart:
