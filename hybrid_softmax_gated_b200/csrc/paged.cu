@@ -34,6 +34,7 @@ constexpr int kMaxHeads = 1024;
 constexpr int kMaxHeadDim = 128;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxCtasPerSm = 8;
+constexpr int kFewRows = 16;  // query rows of a key head up to which the transposed kernel runs
 constexpr long long kMaxKeys = 1ll << 30;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -147,9 +148,14 @@ arl2_status attend_now(arl2_paged_handle* h, const arl2_paged_pool* pool, const 
     a.err = h->err;
     const int max_new = b->max_new > 0 && b->max_new < b->tokens ? b->max_new : b->tokens;
     ++h->launches;
-    const cudaError_t e =
-        h->use_tc ? arl2::launch_paged_tc(h->e4m3, a, h->max_ctas, stream)
-                  : arl2::launch_paged_simt(h->dtype == ARL2_BF16, h->e4m3, a, max_new, h->max_ctas, stream);
+    cudaError_t e;
+    const long long rows = (long long)max_new * h->g.G;
+    if (!h->use_tc)
+        e = arl2::launch_paged_simt(h->dtype == ARL2_BF16, h->e4m3, a, max_new, h->max_ctas, stream);
+    else if (rows <= kFewRows)
+        e = arl2::launch_paged_few(h->e4m3, a, (int)rows, h->max_ctas, stream);
+    else
+        e = arl2::launch_paged_tc(h->e4m3, a, h->max_ctas, stream);
     return e == cudaSuccess ? ARL2_OK : ARL2_ERR_CUDA;
 }
 
@@ -196,7 +202,7 @@ arl2_status arl2_paged_create(const arl2_paged_config* cfg, cudaStream_t stream,
     if (s == ARL2_OK) s = dalloc(h, &h->work.arrived, counters * sizeof(int));
     if (s == ARL2_OK) s = dalloc(h, &h->err, sizeof(int));
     if (s == ARL2_OK && arl2::paged_simt_init() != cudaSuccess) s = ARL2_ERR_CUDA;
-    if (s == ARL2_OK && use_tc && !arl2::paged_tc_init()) s = ARL2_ERR_CUDA;
+    if (s == ARL2_OK && use_tc && !(arl2::paged_tc_init() && arl2::paged_few_init())) s = ARL2_ERR_CUDA;
     if (s == ARL2_OK && (cudaMemsetAsync(h->work.arrived, 0, counters * sizeof(int), stream) != cudaSuccess ||
                          cudaMemsetAsync(h->err, 0, sizeof(int), stream) != cudaSuccess))
         s = ARL2_ERR_CUDA;

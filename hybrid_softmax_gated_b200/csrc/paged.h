@@ -80,5 +80,8 @@ cudaError_t launch_paged_simt(bool bf16, bool e4m3, const PagedAttend& a, int ma
 // bf16 tensors, head width 128, on the tensor cores (paged_tc.cu).
 bool paged_tc_init();
 cudaError_t launch_paged_tc(bool e4m3, const PagedAttend& a, int max_ctas, cudaStream_t st);
+// The same for tiles of `rows` <= 16 query rows (paged_few.cu).
+bool paged_few_init();
+cudaError_t launch_paged_few(bool e4m3, const PagedAttend& a, int rows, int max_ctas, cudaStream_t st);
 
 }  // namespace arl2

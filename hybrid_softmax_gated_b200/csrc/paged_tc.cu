@@ -39,28 +39,29 @@
 // a masked V row holds still enters 0 x v: if that is not finite, O is not,
 // and the rows it hit are computed again with plain loads of the keys they
 // see (repair_row): slow, and only for such rows.
-#include "paged.cuh"
-#include "ptx.cuh"
-#include "tma.h"
+#include "paged_tc.cuh"
 
 #include <cmath>
 
 namespace arl2 {
 namespace {
 
-using ptx::kHalfBytes;
-using ptx::kTileBytes;
+using paged::Desc;
+using paged::kCodeTile;
+using paged::kD;
+using paged::kDescs;
+using paged::kHalfBytes;
+using paged::kKB;
+using paged::kSoftmaxWarps;
+using paged::kTileBytes;
+using paged::kWaitLimitNs;
+using paged::kWgWarps;
 
 constexpr int kRows = 128;  // rows of a half tile
-constexpr int kKB = 128;    // keys per block
-constexpr int kD = 128;
-constexpr int kCodeTile = kKB * kD;  // bytes of a block of codes
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S/P buffers at 0, 128; O_0, O_1 at 256, 384
-constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kSoftmaxWarps = 8, kWgWarps = 4, kConvWarps = 4;
-constexpr int kDescs = 4;
+constexpr int kConvWarps = 4;
 constexpr int kMinUnits = 2;
 
 template <bool kCodes>
@@ -76,22 +77,6 @@ struct Cfg {
     static constexpr int kRegsLow = kCodes ? 72 : 96, kRegsConv = 72, kRegsHigh = kCodes ? 184 : 200;
     static_assert(128 * kRegsLow + 256 * kRegsHigh + (kCodes ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch,
                   "register split");
-};
-
-// What every role needs of a piece of work.
-struct Desc {
-    int done;
-    int s, h, row0, n;       // sequence, key head, first token row, tokens
-    int at0, total;          // position of the first token, keys of the sequence
-    int ns, w0, b0, b1;      // blocks (see Blocks), this CTA's
-    int pair;                // the tile has two halves
-    int c0, c1;              // CTAs that share the tile
-    long long base;
-    // first key of this CTA's block j
-    __device__ int key0(int j) const {
-        const int i = b0 + j;
-        return (i < ns ? i : w0 + i - ns) * kKB;
-    }
 };
 
 template <bool kCodes>
@@ -116,6 +101,14 @@ struct __align__(1024) Smem {
     uint64_t k_full[3], k_empty[3];
     uint64_t v_full[2], v_empty[2];
     uint64_t st_full[2], st_empty[2];
+    // (for the loading warp)
+    static constexpr int kK = C::kK, kKBytes = C::kKBytes, kVLoads = 2;
+    static constexpr uint32_t kQHalf = kHalfBytes;
+    static constexpr bool kClearTail = !kCodes;  // (a code, NaN's too, becomes a finite bf16)
+    __device__ uint64_t* q_landed(int s) { return kCodes ? &q_raw[s] : &q_full[s]; }
+    __device__ uint64_t* v_landed(int s) { return kCodes ? &st_full[s] : &v_full[s]; }
+    __device__ uint64_t* v_taken(int s) { return kCodes ? &st_empty[s] : &v_empty[s]; }
+    __device__ uint8_t* v_load(int s) { return kCodes ? st[s] : v[s]; }
     uint64_t v_tail;             // a ragged block of V has landed, its tail not cleared yet
     uint64_t s_full[2];          // S of warpgroup w's item is in TMEM
     uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the last / first 64 keys written
@@ -145,53 +138,6 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k2p120));
 }
 
-// The first `rows` rows of a Q tile (two swizzled halves of 64 features), in
-// place, into two tiles of e4m3 terms: row r of the halves lies where row r of
-// the terms goes.  16 lanes hold a row.  row_scale: 2^-k scale; NaN for a row
-// that is not finite.
-__device__ __forceinline__ void split_q(uint8_t* tile, float* row_scale, int rows, int cw, float scale) {
-    const int lane = threadIdx.x & 31, c = lane & 15;
-    for (int r0 = cw * 2; r0 < rows; r0 += 8) {
-        const int r = r0 + (lane >> 4);
-        const uint4 u = *reinterpret_cast<const uint4*>(tile + ptx::tile_chunk_offset(r, c));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float x[8], amax = 0.f;
-        bool finite = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-            amax = fmaxf(amax, fabsf(x[i]));
-            finite = finite && fabsf(x[i]) < INFINITY;
-        }
-        if (!finite) amax = INFINITY;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // (every lane has read the row: it may be overwritten)
-        int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);  // amax 2^k in [2^7, 2^8)
-        k = k > 120 ? 120 : k;
-        const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
-        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float2 y = make_float2(x[i] * up, x[i + 1] * up);
-            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-            const __nv_fp8x2_storage_t l =
-                __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
-            hi[i >> 2] |= (uint32_t)h << (8 * (i & 2));
-            lo[i >> 2] |= (uint32_t)l << (8 * (i & 2));
-        }
-        uint8_t* to = tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(to + kHalfBytes) = make_uint2(lo[0], lo[1]);
-        if (c == 0) row_scale[r] = amax < INFINITY ? down * scale : __int_as_float(0x7fffffff);
-    }
-}
-
-__device__ __forceinline__ uint32_t bits_below(int n) {
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 // Row `row` of warpgroup wg's half tile: token of the tile and query head.
 struct RowOf {
     int token, head;
@@ -204,38 +150,6 @@ __device__ __forceinline__ RowOf row_of(const Desc& d, int row, int wg, int G, i
     r.head = d.h * G + row - i * G;
     r.valid = i < HT && r.token < d.n;
     return r;
-}
-
-// One output row again, by a whole warp, with plain loads: O = sum over the
-// keys it sees of the blocks [b0, b1) of exp2(score - m) v, lane l holding
-// features 4 l .. 4 l + 3.  bf16 pages.
-__device__ __noinline__ float4 repair_row(const PagedAttend& a, const Desc& d, int token, int head, float m,
-                                          float scale_log2) {
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16* q =
-        static_cast<const __nv_bfloat16*>(a.q) + (long long)(d.row0 + token) * a.q_stride + head * kD + 4 * lane;
-    float qf[4];
-    for (int c = 0; c < 4; ++c) qf[c] = paged::to_float(q[c]);
-    const paged::Sight see = paged::sight(a.mask, d.at0 + token, d.total);
-    const float base = m == -INFINITY ? 0.f : m;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int bi = d.b0; bi < d.b1; ++bi) {
-        const int key0 = d.key0(bi - d.b0);
-        for (int j = key0; j < key0 + kKB; ++j) {
-            if (!paged::sees(see, j)) continue;
-            const int page = a.seqs.table[(size_t)d.s * a.seqs.max_pages + (j >> a.g.page_log2)];
-            if ((unsigned)page >= (unsigned)a.g.pages) continue;  // (reported by the loader)
-            const size_t at = paged::pool_row(a.g, page, d.h, j) * kD + 4 * lane;
-            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.pool.k) + at;
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool.v) + at;
-            float s = 0.f;
-            for (int c = 0; c < 4; ++c) s = fmaf(qf[c], paged::to_float(k[c]), s);
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float p = ptx::ex2(fmaf(s, scale_log2, -base));
-            for (int c = 0; c < 4; ++c) acc[c] = fmaf(p, paged::to_float(v[c]), acc[c]);
-        }
-    }
-    return make_float4(acc[0], acc[1], acc[2], acc[3]);
 }
 
 template <bool kCodes>
@@ -322,153 +236,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
     if (warp < 4) ptx::setmaxnreg_dec<C::kRegsLow>();
     if (warp == 0) {
         // ------------------------------------------------------ loader --
-        ptx::tma_prefetch_desc(&tm_q);
-        ptx::tma_prefetch_desc(&tm_k);
-        ptx::tma_prefetch_desc(&tm_v);
-        paged::Cursor cur = pl.first;
-        const int page_tokens = 1 << g.page_log2;
-        const int pb_log2 = page_tokens < kKB ? 7 - g.page_log2 : 0;      // pages of a block
-        const int per_block = 1 << pb_log2;
-        const int absent = g.pages * g.Hk;                                // reads as zeros
-        const int batch_log2 = 5 - pb_log2;  // blocks whose pages 32 lanes look up at once
-        int kn = 0, vn = 0, qn = 0, tails = 0;
-        bool ok = true, more = pl.u1 > pl.u0;
-        for (int si = 0; ok; ++si) {
-            const int slot = si % kDescs;
-            if (si >= kDescs && !wwait(&sm.d_empty[slot], (si / kDescs - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            if (!more) {
-                if (lane == 0) sm.desc[slot].done = 1;
-                arrive1(&sm.d_full[slot]);
-                break;
-            }
-            const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, TQ, HT);
-            const bool pair = pc.n > HT;
-            const int at0 = pc.q.total - pc.q.n + pc.i0;
-            if (lane == 0)
-                sm.desc[slot] = Desc{0,          cur.s,        cur.h,        pc.q.q0 + pc.i0, pc.n, at0,
-                                     pc.q.total, pc.blocks.ns, pc.blocks.w0, pc.b0,           pc.b1, pair,
-                                     pc.c0,      pc.c1,        cur.base};
-            arrive1(&sm.d_full[slot]);
-            const int n = pc.b1 - pc.b0;
-            if (n > 0) {
-                for (int t = 0; ok && t < (pair ? 2 : 1); ++t, ++qn) {
-                    const int qs = qn & 1;
-                    if (qn >= 2 && !wwait(&sm.q_empty[qs], ((qn >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = ptx::smem_u32(kCodes ? &sm.q_raw[qs] : &sm.q_full[qs]);
-                    const uint32_t dst = ptx::smem_u32(sm.q[qs]);
-                    ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(HT * g.G) * 256u);
-                    const int row = pc.q.q0 + pc.i0 + t * HT;
-                    ptx::tma_load_4d_w(dst, &tm_q, 0, cur.h * g.G, row, 0, bar);
-                    ptx::tma_load_4d_w(dst + kHalfBytes, &tm_q, 64, cur.h * g.G, row, 0, bar);
-                }
-                // keys that some query of the tile sees: [0, see_sink) and [see_lo, see_end)
-                const paged::Sight last = paged::sight(a.mask, at0 + pc.n - 1, pc.q.total);
-                const int see_lo = paged::sight(a.mask, at0 < 0 ? 0 : at0, pc.q.total).lo;
-                // Places in the pool (page x heads + head, or absent) of a batch of
-                // blocks, one page per lane; a batch is looked up two batches
-                // before it is needed, so nobody waits for the page table.
-                const int span = page_tokens < kKB ? page_tokens : kKB;
-                auto look_up = [&](int b, uint32_t& needed) -> int {
-                    const int j = (b << batch_log2) + (lane >> pb_log2);
-                    const int k0 = pc.blocks.at(pc.b0 + j) * kKB + ((lane & (per_block - 1)) << g.page_log2);
-                    const bool need = j < n && k0 < last.end && (k0 + span > see_lo || k0 < last.sink);
-                    needed = __ballot_sync(0xffffffffu, need);
-                    return need ? a.seqs.table[(size_t)cur.s * a.seqs.max_pages + (k0 >> g.page_log2)] : 0;
-                };
-                uint32_t n0, n1, n2;
-                int b0 = look_up(0, n0), b1 = look_up(1, n1), b2 = look_up(2, n2), b_at = 0;
-                // this lane's place of block j, in batch b_at or the next one
-                auto place_of = [&](int j) -> int {
-                    const bool later = (j >> batch_log2) > b_at;
-                    const int src = ((j << pb_log2) & 31) + (lane & (per_block - 1));
-                    const int page = __shfl_sync(0xffffffffu, later ? b1 : b0, src);
-                    if (lane >= per_block || !(((later ? n1 : n0) >> src) & 1u)) return absent;
-                    if ((unsigned)page < (unsigned)g.pages) return page * g.Hk + cur.h;
-                    paged::report(a.err, kErrPagedTable);
-                    return absent;
-                };
-                auto load_k = [&](int j) -> bool {
-                    const int s = kn % C::kK;
-                    if (kn >= C::kK && !wwait(&sm.k_empty[s], (kn / C::kK - 1) & 1)) return false;
-                    const int place = place_of(j);
-                    const int slot0 = pc.blocks.at(pc.b0 + j) * kKB & (page_tokens - 1);
-                    const uint32_t bar = ptx::smem_u32(&sm.k_full[s]);
-                    const uint32_t there = __popc(__ballot_sync(0xffffffffu, place != absent));
-                    ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)C::kKBytes + (kCodes ? there * (uint32_t)span * 8u : 0u));
-                    __syncwarp();
-                    if (lane < per_block) {
-                        const uint32_t at = (uint32_t)(lane << g.page_log2);  // first row of the page in the tile
-                        const uint32_t dst = ptx::smem_u32(sm.k[s]) + at * 128u;
-                        ptx::tma_load_4d(dst, &tm_k, 0, slot0, place, 0, bar);
-                        if constexpr (kCodes) {
-                            if (place != absent) {
-                                const size_t row = ((size_t)place << g.page_log2) + slot0;
-                                ptx::bulk_load(ptx::smem_u32(sm.ks(kn) + at), a.pool.ks + row, span * 4u, bar);
-                                ptx::bulk_load(ptx::smem_u32(sm.vs(kn) + at), a.pool.vs + row, span * 4u, bar);
-                            }
-                        } else {
-                            ptx::tma_load_4d(dst + kHalfBytes, &tm_k, 64, slot0, place, 0, bar);
-                        }
-                    }
-                    __syncwarp();
-                    ++kn;
-                    return true;
-                };
-                auto load_v = [&](int j) -> bool {
-                    const int s = vn & 1;
-                    if (vn >= 2 && !wwait(kCodes ? &sm.st_empty[s] : &sm.v_empty[s], ((vn >> 1) - 1) & 1)) return false;
-                    const int place = place_of(j);
-                    const int key0 = pc.blocks.at(pc.b0 + j) * kKB;
-                    const int slot0 = key0 & (page_tokens - 1);
-                    uint64_t* full = kCodes ? &sm.st_full[s] : &sm.v_full[s];
-                    if (!kCodes && j == n - 1 && key0 + kKB > pc.q.total) {
-                        full = &sm.v_tail;  // warp 3 clears the tail and hands it on
-                        ++tails;
-                    }
-                    const uint32_t bar = ptx::smem_u32(full);
-                    ptx::mbar_arrive_expect_tx_w(bar, kCodes ? kCodeTile : kTileBytes);
-                    __syncwarp();
-                    if (lane < per_block) {
-                        const uint32_t dst = (kCodes ? ptx::smem_u32(sm.st[s]) : ptx::smem_u32(sm.v[s])) +
-                                             (uint32_t)(lane << g.page_log2) * 128u;
-                        ptx::tma_load_4d(dst, &tm_v, 0, slot0, place, 0, bar);
-                        if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_v, 64, slot0, place, 0, bar);
-                    }
-                    __syncwarp();
-                    ++vn;
-                    return true;
-                };
-                // in the order in which the products take them; the K ring
-                // may be that much ahead
-                for (int j = 0; ok && j < C::kK && j < n; ++j) ok = load_k(j);
-                for (int j = 0; ok && j < n; ++j) {
-                    ok = load_v(j);
-                    if (ok && j + C::kK < n) ok = load_k(j + C::kK);
-                    if (((j + 1) & ((1 << batch_log2) - 1)) == 0) {
-                        b0 = b1, n0 = n1;
-                        b1 = b2, n1 = n2;
-                        ++b_at;
-                        b2 = look_up(b_at + 2, n2);
-                    }
-                }
-            }
-            more = paged::advance(sm.plan, pl, a.seqs, TQ, pc.units, cur);
-        }
-        if (!ok) fail();
-        // the last loads of each ring have landed before exit
-        auto landed = [&](uint64_t* bar, int use) {
-            ptx::mbar_wait_bounded(ptx::smem_u32(bar), use & 1, &no_abort, kWaitLimitNs);
-        };
-        for (int i = kn > C::kK ? kn - C::kK : 0; i < kn; ++i) landed(&sm.k_full[i % C::kK], i / C::kK);
-        if (tails) landed(&sm.v_tail, tails - 1);
-        for (int i = vn > 2 ? vn - 2 : 0; i < vn; ++i) landed(kCodes ? &sm.st_full[i & 1] : &sm.v_full[i & 1], i >> 1);
-        for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i) landed(kCodes ? &sm.q_raw[i & 1] : &sm.q_full[i & 1], i >> 1);
+        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, TQ, HT, wwait)) fail();
     } else if (warp == 1) {
         // ------------------------------------------------------ issuer --
         const uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(kRows, kKB) : ptx::idesc_bf16_f32(kRows, kKB, false, false);
@@ -573,11 +341,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 ++tails;
                 if (!ok) break;
                 const int s = (vn - 1) & 1;  // the piece's last tile
-                const int first = d.total > key0 ? d.total - key0 : 0;
-                for (int half = 0; half < 2; ++half)
-                    for (int at = first * 128 + lane * 16; at < (int)kHalfBytes; at += 512)
-                        *reinterpret_cast<uint4*>(sm.v[s] + half * kHalfBytes + at) = make_uint4(0u, 0u, 0u, 0u);
-                ptx::fence_proxy_async_smem();
+                paged::clear_tail(sm.v[s], 2, key0, d.total);
                 arrive1(&sm.v_full[s]);
             }
             if (!ok) fail();
@@ -603,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                     ok = wwait(&sm.q_raw[qs], (qn >> 1) & 1);
                     if (!ok) break;
                     const int tokens = d.n - t * HT < HT ? d.n - t * HT : HT;
-                    split_q(sm.q[qs], sm.row_scale[qn & 3], tokens * g.G, cw, scale_log2);
+                    paged::split_q<kHalfBytes>(sm.q[qs], sm.row_scale[qn & 3], tokens * g.G, cw, kConvWarps, scale_log2);
                     ptx::fence_proxy_async_smem();
                     arrive1(&sm.q_full[qs]);
                 }
@@ -699,7 +463,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                         uint32_t y[32];
                         ptx::tmem_ld32(sbuf + (uint32_t)c * 32, y);
                         const int k = key0 + 32 * c;
-                        const uint32_t seen = bits_below(see.end - k) & (~bits_below(see.lo - k) | bits_below(see.sink - k));
+                        const uint32_t seen = paged::bits_below(see.end - k) & (~paged::bits_below(see.lo - k) | paged::bits_below(see.sink - k));
                         ptx::tmem_wait_ld();
                         ptx::reg_fence(y);
 #pragma unroll
@@ -755,8 +519,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 ptx::tmem_ld32(sbuf, ya);
                 scaled(yc, 2);
                 scaled(yd, 3);
-                mx = ptx::max3(mx, top(yc), top(yd));
-                mx *= row_mul;
+                mx = ptx::max3(mx, top(yc), top(yd)) * row_mul;
                 const float m_new = fmaxf(m_run, mx);
                 const bool need = m_new > m_run + kRescaleLog2;
                 const float m_use = need ? m_new : m_run;
@@ -918,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                     const int r_head = __shfl_sync(0xffffffffu, head, src);
                     const float r_m = __shfl_sync(0xffffffffu, m, src);
                     const float r_inv = __shfl_sync(0xffffffffu, inv, src);
-                    const float4 o = repair_row(a, d, r_token, r_head, r_m, scale_log2);
+                    const float4 o = paged::repair_row<false>(a, d, r_token, r_head, r_m, scale_log2);
                     if (4 * lane >= col0 && 4 * lane < col0 + 32 * chunks) {
                         if (cut) {
                             part[lane * kRows + src - lane] = o;

@@ -158,8 +158,8 @@ def case_row(case, block, window, sinks):
     key = (id(case), block, window, sinks)
     if key not in _rows:
         _rows.clear()
-        _rows[key] = case.expect(block, window, sinks)
-    return _rows[key]
+        _rows[key] = case, case.expect(block, window, sinks)  # (the case kept alive: its id is not used again)
+    return _rows[key][1]
 
 
 def test_attend_large_scores_stay_finite():
