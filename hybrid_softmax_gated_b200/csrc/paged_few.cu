@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             init(&sm.s_taken[i], kWgWarps);
         }
         for (int i = 0; i < S::kK; ++i) {
-            init(&sm.k_full[i], 1);
+            init(&sm.k_full[i], paged::kKArrivals<kCodes>);
             init(&sm.k_empty[i], 1);
         }
         for (int i = 0; i < S::kVLoads; ++i) {
@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     out[out_at(row) + at] = __float2bfloat16_rn(acc[r] * inv);
                 }
-                if (__any_sync(0xffffffffu, !(acc[r] * 0.f == 0.f))) {
+                // (a row that sees NaN itself has it in its sum: nothing to repair)
+                if (lsum * 0.f == 0.f && __any_sync(0xffffffffu, !(acc[r] * 0.f == 0.f))) {
                     __syncwarp();
                     const int token = row / g.G;
                     const float4 o =

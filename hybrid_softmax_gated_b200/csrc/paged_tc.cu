@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             init(&sm.d_empty[i], 1 + kSoftmaxWarps + (kCodes ? kConvWarps : 1));
         }
         for (int i = 0; i < 3; ++i) {
-            init(&sm.k_full[i], 1);
+            init(&sm.k_full[i], paged::kKArrivals<kCodes>);
             init(&sm.k_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             ptx::tc_fence_before();
             if (n > 0) arrive1(&sm.o_free);
             if constexpr (!kCodes) {
-                uint32_t hurt = __ballot_sync(0xffffffffu, valid && !(zero == 0.f));
+                uint32_t hurt = __ballot_sync(0xffffffffu, valid && !(zero == 0.f) && l * 0.f == 0.f);  // (a NaN sum: the row sees NaN itself)
                 __syncwarp();
                 while (hurt) {
                     const int src = __ffs(hurt) - 1;

@@ -19,6 +19,10 @@ constexpr int kCodeTile = kKB * kD;  // bytes of a block of codes
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr int kSoftmaxWarps = 8, kWgWarps = 4;
 constexpr int kDescs = 4;
+// Arrivals on a K tile's barrier: the loader's and, with codes, its lanes'
+// copies of the scales.
+template <bool kCodes>
+constexpr int kKArrivals = kCodes ? 33 : 1;
 
 // What every role needs of a piece of work.
 struct Desc {
@@ -230,30 +234,24 @@ __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, cons
                 if (kn >= S::kK && !wwait(&sm.k_empty[s], (kn / S::kK - 1) & 1)) return false;
                 const int slot0 = pc.blocks.at(pc.b0 + j) * kKB & (page_tokens - 1);
                 const uint32_t bar = ptx::smem_u32(&sm.k_full[s]);
-                const uint32_t there = __popc(__ballot_sync(0xffffffffu, place != absent));
-                if (kCodes && lane < per_block && place == absent) {  // zeros, as the codes will be
-                    float* ks = sm.ks(kn) + (lane << g.page_log2);
-                    float* vs = sm.vs(kn) + (lane << g.page_log2);
-                    for (int i = 0; i < span; i += 4)
-                        *reinterpret_cast<float4*>(ks + i) = *reinterpret_cast<float4*>(vs + i) =
-                            make_float4(0.f, 0.f, 0.f, 0.f);
+                ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)S::kKBytes);
+                if constexpr (kCodes) {
+                    // the scales: 16 bytes per lane and tensor (bulk copies of a
+                    // page's scales cost the copy engine as much as its codes:
+                    // 236 against 191 us without them at 64 streams of 8256 keys)
+                    const int of = ((4 * lane) >> g.page_log2) & (per_block - 1);
+                    const int there = __shfl_sync(0xffffffffu, place, of);
+                    const size_t row = there == absent ? 0 : ((size_t)there << g.page_log2) + slot0 + 4 * lane - (of << g.page_log2);
+                    const uint32_t bytes = there == absent ? 0u : 16u;  // (absent: zeros, as the codes will be)
+                    ptx::cp_async16(ptx::smem_u32(sm.ks(kn) + 4 * lane), a.pool.ks + row, bytes);
+                    ptx::cp_async16(ptx::smem_u32(sm.vs(kn) + 4 * lane), a.pool.vs + row, bytes);
+                    ptx::cp_async_arrive(bar);
                 }
                 __syncwarp();
-                ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)S::kKBytes + (kCodes ? there * (uint32_t)span * 8u : 0u));
-                __syncwarp();
                 if (lane < per_block) {
-                    const uint32_t at = (uint32_t)(lane << g.page_log2);  // first row of the page in the tile
-                    const uint32_t dst = ptx::smem_u32(sm.k[s]) + at * 128u;
+                    const uint32_t dst = ptx::smem_u32(sm.k[s]) + (uint32_t)(lane << g.page_log2) * 128u;
                     ptx::tma_load_4d(dst, &tm_k, 0, slot0, place, 0, bar);
-                    if constexpr (kCodes) {
-                        if (place != absent) {
-                            const size_t row = ((size_t)place << g.page_log2) + slot0;
-                            ptx::bulk_load(ptx::smem_u32(sm.ks(kn) + at), a.pool.ks + row, span * 4u, bar);
-                            ptx::bulk_load(ptx::smem_u32(sm.vs(kn) + at), a.pool.vs + row, span * 4u, bar);
-                        }
-                    } else {
-                        ptx::tma_load_4d(dst + kHalfBytes, &tm_k, 64, slot0, place, 0, bar);
-                    }
+                    if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_k, 64, slot0, place, 0, bar);
                 }
                 __syncwarp();
                 ++kn;
