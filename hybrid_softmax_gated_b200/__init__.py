@@ -180,8 +180,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current device's current stream (its handle alone: a Stream object costs 5 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -550,19 +550,20 @@ def _dtype(t: torch.dtype) -> int:
 def _head_rows(t, name, heads, d, dtype, device, tokens=None):
     """A [tokens, heads, d] tensor whose tokens may be strided (a slice of a
     joint qkv projection); returns it."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (tokens is not None and t.shape[0] != tokens):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, {heads}, {d}]")
     if t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor of the layer's dtype and device")
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)
-                      or (t.shape[0] > 1 and t.stride(0) < heads * d)):
+    if not t.is_contiguous() and t.numel() and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)
+                                                or (shape[0] > 1 and t.stride(0) < heads * d)):
         raise ValueError(f"{name} must have contiguous heads (tokens may be strided)")
     return t
 
 
 def _token_stride(t) -> int:
     # (the stride of a single token says nothing: dense)
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return 0 if t.is_contiguous() or t.shape[0] <= 1 else t.stride(0)
 
 
 def _table(t, name, shape, device):
@@ -573,13 +574,16 @@ def _table(t, name, shape, device):
     return t
 
 
-def _new(like, shape, dtype, stream):
-    """An output of this call; the allocator is told when it is used on another
-    stream than the current one."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if isinstance(stream, torch.cuda.Stream) and stream != torch.cuda.current_stream(like.device):
+def _used(t, stream):
+    """t, an output of this call; the allocator is told when it is used on
+    another stream than the current one."""
+    if isinstance(stream, torch.cuda.Stream) and stream != torch.cuda.current_stream(t.device):
         t.record_stream(stream)
     return t
+
+
+def _like(t, stream):
+    return _used(torch.empty_like(t, memory_format=torch.contiguous_format), stream)
 
 
 class RotaryAxes:
@@ -613,33 +617,33 @@ class RotaryAxes:
         """(q, k) turned by positions (int32 [tokens, axes]): [tokens, heads, d]
         each, k may be None.  inverse turns back, which is also the gradient.
         q_out, k_out may be q, k (in place)."""
-        tokens, d = q.shape[0], self.head_dim
         if not q.is_cuda:
             raise ValueError("q must be a CUDA tensor")
-        dt = _dtype(q.dtype)
-        _head_rows(q, "q", q.shape[1] if q.dim() == 3 else 0, d, q.dtype, q.device)
-        _table(positions, "positions", (tokens, self.axes), q.device)
+        d, shape, dtype, device = self.head_dim, q.shape, q.dtype, q.device
+        tokens, qh = (shape[0], shape[1]) if len(shape) == 3 else (0, 0)
+        dt = _dtype(dtype)
+        _head_rows(q, "q", qh, d, dtype, device)
+        _table(positions, "positions", (tokens, self.axes), device)
         if q_out is None:
-            q_out = _new(q, q.shape, q.dtype, stream)
+            q_out = _like(q, stream)
         else:
-            _head_rows(q_out, "q_out", q.shape[1], d, q.dtype, q.device, tokens)
-        kh, ks, kos = 0, 0, 0
+            _head_rows(q_out, "q_out", qh, d, dtype, device, tokens)
+        kh, ks, kos, kp, kop = 0, 0, 0, None, None
         if k is None:
             k_out = None
         else:
             kh = k.shape[1] if k.dim() == 3 else 0
-            _head_rows(k, "k", kh, d, q.dtype, q.device, tokens)
+            _head_rows(k, "k", kh, d, dtype, device, tokens)
             if k_out is None:
-                k_out = _new(k, k.shape, k.dtype, stream)
+                k_out = _like(k, stream)
             else:
-                _head_rows(k_out, "k_out", kh, d, q.dtype, q.device, tokens)
-            ks, kos = _token_stride(k), _token_stride(k_out)
-        if q.device.index != torch.cuda.current_device():
+                _head_rows(k_out, "k_out", kh, d, dtype, device, tokens)
+            ks, kos, kp, kop = _token_stride(k), _token_stride(k_out), k.data_ptr(), k_out.data_ptr()
+        if device.index != torch._C._cuda_getDevice():
             raise Arl2Error(-1, "arl2_rotary_apply: the current device is not the tensors'")
-        _check(_lib.arl2_rotary_apply(self.handle, dt, tokens, positions.data_ptr(), q.shape[1], q.data_ptr(),
-                                      _token_stride(q), q_out.data_ptr(), _token_stride(q_out), kh,
-                                      None if k is None else k.data_ptr(), ks,
-                                      None if k is None else k_out.data_ptr(), kos, 1 if inverse else 0,
+        _check(_lib.arl2_rotary_apply(self.handle, dt, tokens, positions.data_ptr(), qh, q.data_ptr(),
+                                      _token_stride(q), q_out.data_ptr(), _token_stride(q_out), kh, kp, ks, kop, kos,
+                                      1 if inverse else 0,
                                       _stream(stream)), "arl2_rotary_apply")
         return q_out, k_out
 
@@ -753,7 +757,7 @@ class PagedCache:
 
     def _out(self, out, q, stream):
         if out is None:
-            return _new(q, q.shape, q.dtype, stream)
+            return _like(q, stream)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
         return self._rows(out, "out", 0, q.shape[0])
@@ -779,7 +783,7 @@ class PagedCache:
         outs = []
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             if t is None:
-                t = _new(page_table, shape, self.dtype, stream)
+                t = _used(torch.empty(shape, dtype=self.dtype, device=self.device), stream)
             elif not self._rows(t, name, 1, tokens).is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
             outs.append(t)
@@ -815,7 +819,8 @@ class PagedCache:
             if positions is None or rotary.head_dim != self.head_dim:
                 raise ValueError("rotary needs positions and the cache's head_dim")
             _table(positions, "positions", (tokens, rotary.axes), self.device)
-            turned = _new(q, (tokens, sum(self.heads), self.head_dim), self.dtype, stream)
+            turned = _used(torch.empty((tokens, sum(self.heads), self.head_dim), dtype=self.dtype, device=self.device),
+                           stream)
         out = self._out(out, q, stream)
         _check(_lib.arl2_paged_forward(self.handle, self._pool(layer), self._batch(batch, tokens),
                                        None if rotary is None else rotary.handle,

@@ -6,74 +6,79 @@
 // read once and written once.  A row is held by 16 lanes (bf16, d = 128) or
 // 32 (fp32), 16 bytes each, so its largest magnitude takes four or five
 // shuffles and never leaves the registers.  Widths that do not fit take the
-// generic form, a warp per row.  A block takes a few tokens with all their
-// heads of both tensors: the sequence a token belongs to and its page are
-// looked up once per token.
+// generic form, a warp per row.  A warp takes a few rows of one token, all
+// their loads in flight together; it finds the token's sequence by a 32-way
+// search of the offsets (one load for up to 32 sequences, two for 1024).
 #include "paged.cuh"
+
+#include <type_traits>
 
 namespace arl2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 8;  // tokens per block
+constexpr int kSteps = 4;  // rows a lane has in flight
 constexpr float kCodeMax = 448.f, kScaleMin = 0x1p-126f;
 
-// Sequence of row `tok`: the number of offsets in (offsets[0], offsets[S]]
-// that are <= tok, counted by the whole block (offsets ascend).
+// Sequence of row `tok`: how many of the ascending offsets[1 .. S] are <= tok.
+// The whole warp, S <= 1024.
 __device__ __forceinline__ int owner_of(const int* __restrict__ offsets, int S, int tok) {
-    int s = 0;
-    for (int i0 = 0; i0 < S; i0 += kThreads) {
-        const int i = i0 + threadIdx.x;
-        s += __syncthreads_count(i < S && offsets[i + 1] <= tok);
+    const int lane = threadIdx.x & 31;
+    int first = 0;
+    if (S > 32) {  // the group of 32 that the answer lies in
+        const int i = 32 * lane + 32;
+        first = 32 * __popc(__ballot_sync(0xffffffffu, i <= S && offsets[i] <= tok));
     }
-    return s;
+    const int i = first + lane + 1;
+    return first + __popc(__ballot_sync(0xffffffffu, i <= S && offsets[i] <= tok));
 }
 
-// Place of each of the block's tokens: page and key position, or page -1.
-struct Places {
-    int page[kMaxTok], key[kMaxTok];
+// Place of a token in the cache: page and key position, or page -1.
+struct Place {
+    int page, key;
 };
 
 // Writing: row i of a sequence's n is its position total - n + i; reading:
-// starts[s] + i (starts == nullptr: i).
-__device__ __forceinline__ void find_places(const PagedGeom& g, const PagedSeqs& b, const int* starts, bool reading,
-                                            int tok0, int n_tok, Places& pl, int* err) {
-    int s = 0;  // thread t looks up the block's token t
-    for (int t = 0; t < n_tok; ++t) {
-        const int o = owner_of(b.q_off, b.S, tok0 + t);
-        if ((int)threadIdx.x == t) s = o;
+// starts[s] + i (starts == nullptr: i).  The whole warp.
+__device__ __forceinline__ Place find_place(const PagedGeom& g, const PagedSeqs& b, const int* starts, bool reading,
+                                            int tok, int* err) {
+    const int s = owner_of(b.q_off, b.S, tok);
+    Place pl{-1, 0};
+    if (s >= b.S || tok < b.q_off[0]) return pl;
+    const long long cap = (long long)b.max_pages << g.page_log2;
+    const int q0 = b.q_off[s], q1 = b.q_off[s + 1];
+    long long at;
+    bool bad = q0 < 0 || q1 < q0 || q1 > b.tokens;
+    if (reading) {
+        at = (long long)(starts ? starts[s] : 0) + (tok - q0);
+        bad = bad || at < 0 || at >= cap;
+    } else {
+        const int total = b.kv_len[s];
+        bad = bad || total < 0 || total > cap;
+        at = (long long)total - (q1 - q0) + (tok - q0);
     }
-    if ((int)threadIdx.x < n_tok) {
-        const int tok = tok0 + threadIdx.x;
-        int page = -1, key = 0;
-        if (s < b.S && tok >= b.q_off[0]) {
-            const long long cap = (long long)b.max_pages << g.page_log2;
-            const int q0 = b.q_off[s], q1 = b.q_off[s + 1];
-            long long at;
-            bool bad = q0 < 0 || q1 < q0 || q1 > b.tokens;
-            if (reading) {
-                at = (long long)(starts ? starts[s] : 0) + (tok - q0);
-                bad = bad || at < 0 || at >= cap;
-            } else {
-                const int total = b.kv_len[s];
-                bad = bad || total < 0 || total > cap;
-                at = (long long)total - (q1 - q0) + (tok - q0);
-            }
-            if (bad) {
-                paged::report(err, kErrPagedTable);
-            } else if (at >= 0) {  // (before position 0: a chunk padded on the left)
-                key = (int)at;
-                page = b.table[(size_t)s * b.max_pages + (key >> g.page_log2)];
-                if ((unsigned)page >= (unsigned)g.pages) {
-                    paged::report(err, kErrPagedTable);
-                    page = -1;
-                }
-            }
-        }
-        pl.page[threadIdx.x] = page;
-        pl.key[threadIdx.x] = key;
+    if (bad) {
+        paged::report(err, kErrPagedTable);
+    } else if (at >= 0) {  // (before position 0: a chunk padded on the left)
+        const int page = b.table[(size_t)s * b.max_pages + ((int)at >> g.page_log2)];
+        if ((unsigned)page < (unsigned)g.pages)
+            pl = Place{page, (int)at};
+        else
+            paged::report(err, kErrPagedTable);
     }
-    __syncthreads();
+    return pl;
+}
+
+// The warp's share of the tokens' rows (K's heads, then V's): kSteps steps of
+// kPer rows of one token.
+struct Share {
+    int tok, r0;  // token, first row
+};
+__device__ __forceinline__ Share share_of(int rows, int per_warp) {
+    const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int parts = (rows + per_warp - 1) / per_warp;
+    const long long tok = w / parts;
+    return Share{(int)tok, (int)(w - tok * parts) * per_warp};
 }
 
 template <typename T>
@@ -81,8 +86,7 @@ struct Lane16;  // elements of 16 bytes
 template <>
 struct Lane16<__nv_bfloat16> {
     static constexpr int n = 8;
-    static __device__ __forceinline__ void load(const void* p, float (&x)[8]) {
-        const uint4 u = __ldcs(static_cast<const uint4*>(p));
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -103,9 +107,9 @@ struct Lane16<__nv_bfloat16> {
 template <>
 struct Lane16<float> {
     static constexpr int n = 4;
-    static __device__ __forceinline__ void load(const void* p, float (&x)[4]) {
-        const float4 u = __ldcs(static_cast<const float4*>(p));
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
     }
     static __device__ __forceinline__ void store(void* p, const float (&x)[4]) {
         __stcs(static_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
@@ -128,37 +132,36 @@ __device__ __forceinline__ float scale_of(float amax, bool finite) {
 // kLanes lanes hold a row (d = kLanes * Lane16<T>::n); 0: the generic form.
 template <typename T, bool kCodes, int kLanes>
 __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool pool, PagedSeqs b, const T* k,
-                                                         long long k_stride, const T* v, long long v_stride,
-                                                         int per_block, int* err) {
-    __shared__ Places pl;
-    const int tok0 = blockIdx.x * per_block;
-    const int n_tok = min(per_block, b.tokens - tok0);
-    find_places(g, b, nullptr, false, tok0, n_tok, pl, err);
-    constexpr int kRow = kLanes ? kLanes : 32;
-    const int lane = threadIdx.x % kRow;
-    const int rows = n_tok * 2 * g.Hk;
-    for (int r0 = 0; r0 < rows; r0 += kThreads / kRow) {  // (whole warps: the shuffles need every lane)
-        const int r = r0 + threadIdx.x / kRow;
-        const int t = r < rows ? r / (2 * g.Hk) : 0;
-        const int hh = r - t * 2 * g.Hk;
-        const bool is_v = hh >= g.Hk;
-        const int h = is_v ? hh - g.Hk : hh;
-        const bool on = r < rows && pl.page[t] >= 0;
-        const T* src = (is_v ? v + (long long)(tok0 + t) * v_stride : k + (long long)(tok0 + t) * k_stride) + h * g.d;
-        const size_t row = on ? paged::pool_row(g, pl.page[t], h, pl.key[t]) : 0;
-        void* dst = is_v ? pool.v : pool.k;
-        float* sc = is_v ? pool.vs : pool.ks;
-        if constexpr (kLanes > 0) {
-            constexpr int n = Lane16<T>::n;
+                                                         long long k_stride, const T* v, long long v_stride, int* err) {
+    constexpr int kRow = kLanes ? kLanes : 32, kPer = 32 / kRow;
+    const int rows = 2 * g.Hk;
+    const Share sh = share_of(rows, kSteps * kPer);
+    if (sh.tok >= b.tokens) return;
+    const int lane = threadIdx.x & 31, c = lane % kRow, sub = lane / kRow;
+    auto source = [&](int r) {
+        return r >= g.Hk ? v + sh.tok * v_stride + (long long)(r - g.Hk) * g.d : k + sh.tok * k_stride + (long long)r * g.d;
+    };
+    if constexpr (kLanes > 0) {
+        constexpr int n = Lane16<T>::n;
+        uint4 raw[kSteps];  // (the rows' loads do not wait for their place)
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int r = sh.r0 + u * kPer + sub;
+            raw[u] = r < rows ? __ldcs(reinterpret_cast<const uint4*>(source(r)) + c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        const Place pl = find_place(g, b, nullptr, false, sh.tok, err);
+        if (pl.page < 0) return;
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int r = sh.r0 + u * kPer + sub;
+            const bool on = r < rows, is_v = r >= g.Hk;
+            const size_t row = on ? paged::pool_row(g, pl.page, is_v ? r - g.Hk : r, pl.key) : 0;
+            void* dst = is_v ? pool.v : pool.k;
             if constexpr (!kCodes) {
-                if (on)
-                    reinterpret_cast<uint4*>(dst)[row * kLanes + lane] =
-                        __ldcs(reinterpret_cast<const uint4*>(src) + lane);
+                if (on) reinterpret_cast<uint4*>(dst)[row * kLanes + c] = raw[u];
             } else {
                 float x[n];
-#pragma unroll
-                for (int i = 0; i < n; ++i) x[i] = 0.f;
-                if (on) Lane16<T>::load(reinterpret_cast<const uint4*>(src) + lane, x);
+                Lane16<T>::unpack(raw[u], x);
                 float amax = 0.f;
                 bool finite = true;
 #pragma unroll
@@ -176,44 +179,48 @@ __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool 
                     uint32_t w[n / 4];
 #pragma unroll
                     for (int i = 0; i < n / 4; ++i) {
-                        uint32_t c = 0;
+                        uint32_t code = 0;
 #pragma unroll
                         for (int j = 0; j < 4; j += 2) {
                             const float2 y = make_float2(x[4 * i + j] * inv, x[4 * i + j + 1] * inv);
-                            c |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (8 * j);
+                            code |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (8 * j);
                         }
-                        w[i] = finite ? c : 0u;
+                        w[i] = finite ? code : 0u;
                     }
-                    uint32_t* to = reinterpret_cast<uint32_t*>(dst) + (row * kLanes + lane) * (n / 4);
+                    uint32_t* to = reinterpret_cast<uint32_t*>(dst) + (row * kLanes + c) * (n / 4);
                     if constexpr (n == 8)
                         *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
                     else
                         *to = w[0];
-                    if (lane == 0) sc[row] = s;
+                    if (c == 0) (is_v ? pool.vs : pool.ks)[row] = s;
                 }
             }
-        } else {
+        }
+    } else {
+        const Place pl = find_place(g, b, nullptr, false, sh.tok, err);
+        if (pl.page < 0) return;
+        for (int r = sh.r0; r < sh.r0 + kSteps && r < rows; ++r) {
+            const bool is_v = r >= g.Hk;
+            const T* src = source(r);
+            const size_t row = paged::pool_row(g, pl.page, is_v ? r - g.Hk : r, pl.key);
+            void* dst = is_v ? pool.v : pool.k;
             if constexpr (!kCodes) {
-                if (on)
-                    for (int c = lane; c < g.d; c += 32) static_cast<T*>(dst)[row * g.d + c] = src[c];
+                for (int i = lane; i < g.d; i += 32) static_cast<T*>(dst)[row * g.d + i] = src[i];
             } else {
                 float amax = 0.f;
-                if (on)
-                    for (int c = lane; c < g.d; c += 32) {
-                        const float a = fabsf(paged::to_float(src[c]));
-                        amax = a < INFINITY ? fmaxf(amax, a) : INFINITY;
-                    }
+                for (int i = lane; i < g.d; i += 32) {
+                    const float x = fabsf(paged::to_float(src[i]));
+                    amax = x < INFINITY ? fmaxf(amax, x) : INFINITY;
+                }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 const bool finite = amax < INFINITY;
                 const float s = scale_of(amax, finite);
-                if (on) {
-                    const float inv = 1.f / s;
-                    for (int c = lane; c < g.d; c += 32)
-                        static_cast<unsigned char*>(dst)[row * g.d + c] =
-                            finite ? code_of(paged::to_float(src[c]) * inv) : (unsigned char)0;
-                    if (lane == 0) sc[row] = s;
-                }
+                const float inv = 1.f / s;
+                for (int i = lane; i < g.d; i += 32)
+                    static_cast<unsigned char*>(dst)[row * g.d + i] =
+                        finite ? code_of(paged::to_float(src[i]) * inv) : (unsigned char)0;
+                if (lane == 0) (is_v ? pool.vs : pool.ks)[row] = s;
             }
         }
     }
@@ -221,55 +228,69 @@ __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool 
 
 template <typename T, bool kCodes, int kLanes>
 __global__ void __launch_bounds__(kThreads) read_kernel(PagedGeom g, PagedPool pool, PagedSeqs b, const int* starts,
-                                                        T* k, T* v, int per_block, int* err) {
-    __shared__ Places pl;
-    const int tok0 = blockIdx.x * per_block;
-    const int n_tok = min(per_block, b.tokens - tok0);
-    find_places(g, b, starts, true, tok0, n_tok, pl, err);
-    constexpr int kRow = kLanes ? kLanes : 32;
-    const int lane = threadIdx.x % kRow;
-    const int rows = n_tok * 2 * g.Hk;
-#pragma unroll 4
-    for (int r = threadIdx.x / kRow; r < rows; r += kThreads / kRow) {
-        const int t = r / (2 * g.Hk);
-        const int hh = r - t * 2 * g.Hk;
-        const bool is_v = hh >= g.Hk;
-        const int h = is_v ? hh - g.Hk : hh;
-        if (pl.page[t] < 0) continue;
-        const size_t row = paged::pool_row(g, pl.page[t], h, pl.key[t]);
-        const void* src = is_v ? pool.v : pool.k;
-        T* dst = (is_v ? v : k) + ((size_t)(tok0 + t) * g.Hk + h) * g.d;
-        const float s = kCodes ? __ldg((is_v ? pool.vs : pool.ks) + row) : 1.f;
-        if constexpr (kLanes > 0) {
-            constexpr int n = Lane16<T>::n;
+                                                        T* k, T* v, int* err) {
+    constexpr int kRow = kLanes ? kLanes : 32, kPer = 32 / kRow;
+    const int rows = 2 * g.Hk;
+    const Share sh = share_of(rows, kSteps * kPer);
+    if (sh.tok >= b.tokens) return;
+    const int lane = threadIdx.x & 31, c = lane % kRow, sub = lane / kRow;
+    const Place pl = find_place(g, b, starts, true, sh.tok, err);
+    if (pl.page < 0) return;
+    auto row_at = [&](int r) { return paged::pool_row(g, pl.page, r >= g.Hk ? r - g.Hk : r, pl.key); };
+    auto target = [&](int r) {
+        return r >= g.Hk ? v + ((size_t)sh.tok * g.Hk + r - g.Hk) * g.d : k + ((size_t)sh.tok * g.Hk + r) * g.d;
+    };
+    if constexpr (kLanes > 0) {
+        constexpr int n = Lane16<T>::n;
+        using Raw = typename std::conditional<!kCodes, uint4, typename std::conditional<n == 8, uint2, uint32_t>::type>::type;
+        Raw raw[kSteps];
+        float s[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int r = sh.r0 + u * kPer + sub;
+            if (r < rows) {
+                const bool is_v = r >= g.Hk;
+                raw[u] = __ldcs(static_cast<const Raw*>(is_v ? pool.v : pool.k) + row_at(r) * kLanes + c);
+                s[u] = kCodes ? __ldg((is_v ? pool.vs : pool.ks) + row_at(r)) : 1.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int r = sh.r0 + u * kPer + sub;
+            if (r >= rows) continue;
+            uint4* to = reinterpret_cast<uint4*>(target(r)) + c;
             if constexpr (!kCodes) {
-                __stcs(reinterpret_cast<uint4*>(dst) + lane, __ldcs(static_cast<const uint4*>(src) + row * kLanes + lane));
+                __stcs(to, raw[u]);
             } else {
                 uint32_t w[n / 4];
-                const uint32_t* from = static_cast<const uint32_t*>(src) + (row * kLanes + lane) * (n / 4);
-                if constexpr (n == 8) {
-                    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(from));
-                    w[0] = u.x, w[1] = u.y;
-                } else {
-                    w[0] = __ldcs(from);
-                }
+                if constexpr (n == 8)
+                    w[0] = raw[u].x, w[1] = raw[u].y;
+                else
+                    w[0] = raw[u];
                 float x[n];
 #pragma unroll
                 for (int i = 0; i < n; i += 2) {
                     const __half2_raw hr =
                         __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 4] >> (8 * (i % 4))), __NV_E4M3);
                     const float2 f = __half22float2(__half2(hr));
-                    x[i] = f.x * s;
-                    x[i + 1] = f.y * s;
+                    x[i] = f.x * s[u];
+                    x[i + 1] = f.y * s[u];
                 }
-                Lane16<T>::store(reinterpret_cast<uint4*>(dst) + lane, x);
+                Lane16<T>::store(to, x);
             }
-        } else {
-            for (int c = lane; c < g.d; c += 32) {
+        }
+    } else {
+        for (int r = sh.r0; r < sh.r0 + kSteps && r < rows; ++r) {
+            const size_t row = row_at(r);
+            const bool is_v = r >= g.Hk;
+            const void* src = is_v ? pool.v : pool.k;
+            const float s = kCodes ? (is_v ? pool.vs : pool.ks)[row] : 1.f;
+            T* dst = target(r);
+            for (int i = lane; i < g.d; i += 32) {
                 if constexpr (kCodes)
-                    paged::store_as(dst + c, value_of(static_cast<const unsigned char*>(src)[row * g.d + c]) * s);
+                    paged::store_as(dst + i, value_of(static_cast<const unsigned char*>(src)[row * g.d + i]) * s);
                 else
-                    dst[c] = static_cast<const T*>(src)[row * g.d + c];
+                    dst[i] = static_cast<const T*>(src)[row * g.d + i];
             }
         }
     }
@@ -277,38 +298,40 @@ __global__ void __launch_bounds__(kThreads) read_kernel(PagedGeom g, PagedPool p
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// As many tokens per block as still leave several blocks per SM.
-int tokens_per_block(int tokens) { return tokens >= 148 * 8 * 8 ? 8 : tokens >= 148 * 4 * 4 ? 4 : tokens >= 148 * 4 ? 2 : 1; }
+// Blocks for the tokens' rows, `per` rows a step.
+unsigned blocks_for(int tokens, int Hk, int per) {
+    const int parts = (2 * Hk + kSteps * per - 1) / (kSteps * per);
+    return (unsigned)(((long long)tokens * parts + kThreads / 32 - 1) / (kThreads / 32));
+}
 
 template <typename T, bool kCodes>
 cudaError_t write_as(const PagedGeom& g, const PagedPool& pool, const PagedSeqs& b, const void* k, long long ks,
                      const void* v, long long vs, int* err, cudaStream_t st) {
     constexpr int n = Lane16<T>::n;
-    const int per = tokens_per_block(b.tokens), grid = (b.tokens + per - 1) / per;
     const bool fits = aligned16(k) && aligned16(v) && ks % n == 0 && vs % n == 0;
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kThreads, 0, st>>>(g, pool, b, static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, per,
-                                          err);
+    auto go = [&](auto kernel, int lanes) {
+        kernel<<<blocks_for(b.tokens, g.Hk, 32 / lanes), kThreads, 0, st>>>(g, pool, b, static_cast<const T*>(k), ks,
+                                                                          static_cast<const T*>(v), vs, err);
         return cudaGetLastError();
     };
-    if (fits && g.d == 128) return go(write_kernel<T, kCodes, 128 / n>);
-    if (fits && g.d == 64) return go(write_kernel<T, kCodes, 64 / n>);
-    return go(write_kernel<T, kCodes, 0>);
+    if (fits && g.d == 128) return go(write_kernel<T, kCodes, 128 / n>, 128 / n);
+    if (fits && g.d == 64) return go(write_kernel<T, kCodes, 64 / n>, 64 / n);
+    return go(write_kernel<T, kCodes, 0>, 32);
 }
 
 template <typename T, bool kCodes>
 cudaError_t read_as(const PagedGeom& g, const PagedPool& pool, const PagedSeqs& b, const int* starts, void* k, void* v,
                     int* err, cudaStream_t st) {
     constexpr int n = Lane16<T>::n;
-    const int per = tokens_per_block(b.tokens), grid = (b.tokens + per - 1) / per;
     const bool fits = aligned16(k) && aligned16(v);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kThreads, 0, st>>>(g, pool, b, starts, static_cast<T*>(k), static_cast<T*>(v), per, err);
+    auto go = [&](auto kernel, int lanes) {
+        kernel<<<blocks_for(b.tokens, g.Hk, 32 / lanes), kThreads, 0, st>>>(g, pool, b, starts, static_cast<T*>(k),
+                                                                          static_cast<T*>(v), err);
         return cudaGetLastError();
     };
-    if (fits && g.d == 128) return go(read_kernel<T, kCodes, 128 / n>);
-    if (fits && g.d == 64) return go(read_kernel<T, kCodes, 64 / n>);
-    return go(read_kernel<T, kCodes, 0>);
+    if (fits && g.d == 128) return go(read_kernel<T, kCodes, 128 / n>, 128 / n);
+    if (fits && g.d == 64) return go(read_kernel<T, kCodes, 64 / n>, 64 / n);
+    return go(read_kernel<T, kCodes, 0>, 32);
 }
 
 }  // namespace
