@@ -7,11 +7,10 @@
 // own rounding (2^-65 turns per position step): no range reduction, and a
 // position of 10^6 costs no accuracy.  Its top part goes through sincospif.
 //
-// Memory bound: q and k are read once and written once.  A thread keeps one
-// place of a head (a 16-byte vector of features) and one token, works out its
-// few pairs' sines once, in registers, and turns that place of the token's
-// heads, four loads in flight.  Few tokens: a token's heads are split over
-// more threads.  14400 tokens of 24 heads (177 MB in all): 32 us, 5.5 TB/s.
+// Memory bound: q and k are read once and written once.  A thread has one
+// place of a head (16 bytes of features, or two) and up to four heads of one
+// token; its loads are on their way while the block works out its tokens'
+// sines, once each, into shared memory.
 #include "arl2.h"
 #include "internal.h"
 
@@ -24,7 +23,8 @@ namespace {
 
 constexpr int kMaxPairs = 128;
 constexpr int kThreads = 256;
-constexpr int kInFlight = 4;  // heads a thread loads before it turns them
+constexpr int kMaxTokensPerBlock = 32;
+constexpr int kInFlight = 4;  // heads of an item, all their loads on their way together
 
 // The plan as the kernel gets it (1.2 KB of launch parameters).
 struct Plan {
@@ -40,128 +40,188 @@ struct Side {
     int heads;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x) {
-    return static_cast<float>(x);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
+// A place of a head: what an item turns, 16 bytes of it (kHalves: 16 bytes of
+// each half), or, with kWide = false, one pair in single elements: the form
+// for heads, strides or pointers that 16-byte vectors do not fit.  kHalves:
+// pair p = features (p, p + R/2), else (2p, 2p + 1).
+template <typename T, bool kHalves, bool kWide>
+struct Form {
+    static constexpr int kBytes = kWide ? 16 : (int)sizeof(T);  // of a load
+    static constexpr int NP = kWide ? (kHalves ? 16 : 8) / (int)sizeof(T) : 1;
+    static constexpr int kLoads = !kWide ? 2 : kHalves ? 2 : 1;
+    static constexpr int kStep = kHalves || !kWide ? kBytes / (int)sizeof(T) : 2 * NP;  // features from place to place
+    static constexpr int kTail = kBytes / (int)sizeof(T);  // untouched features of an item behind the turned ones
+};
+template <int kBytes>
+struct RawOf;
 template <>
-__device__ __forceinline__ float from_f<float>(float x) {
-    return x;
-}
+struct RawOf<16> {
+    using type = uint4;
+};
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
-}
-
-template <typename T, int N, int kAlign>
-struct __align__(kAlign) Vec {
-    T v[N];
+struct RawOf<4> {
+    using type = uint32_t;
+};
+template <>
+struct RawOf<2> {
+    using type = uint16_t;
 };
 
-// A thread's place of a head: NP pairs, or (past the turned features) kTail
-// elements copied through.  kHalves: pair p = features (p, p + R/2).  NP = 1
-// is the form for heads, strides or pointers that 16-byte vectors do not
-// fit: it touches single elements.  `split` threads share the heads of a place.
-template <typename T, bool kHalves, int NP>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Plan plan, Side q, Side k,
-                                                          const int* __restrict__ positions, int tokens, int split,
-                                                          float sign) {
-    constexpr int N = kHalves ? NP : 2 * NP;  // elements of one vector
-    constexpr int kTail = NP == 1 ? 1 : N;
-    using V = Vec<T, N, NP == 1 ? sizeof(T) : 16>;
-    using Tail = Vec<T, kTail, NP == 1 ? sizeof(T) : 16>;
-    const int half = plan.rot >> 1;
-    const int turned = half / NP;  // places that turn
-    const int per_head = turned + (plan.d - plan.rot) / kTail;
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    // (a division of 64-bit numbers costs more than all of a place's sines)
-    const bool small = i < (1ll << 32);
-    const long long hs = small ? (unsigned)i / (unsigned)per_head : i / per_head;
-    const int e = (int)(i - hs * per_head);
-    const long long tok = small ? (unsigned)hs / (unsigned)split : hs / split;
-    const int h0 = (int)(hs - tok * split);
-    if (tok >= tokens) return;
-    const int heads = q.heads + k.heads;
-    const bool turns = e < turned;
-    float c[NP], s[NP];
-    if (turns) {
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            const int p = e * NP + j;
-            const long long pos = positions[tok * plan.axes + plan.axis[p]];
-            const long long phase = (long long)((unsigned long long)pos * plan.freq[p]);
-            sincospif(__ll2float_rn(phase) * 0x1p-63f, &s[j], &c[j]);
-            s[j] *= sign;
-        }
+// (written out, so that every form of the kernel rounds alike)
+__device__ __forceinline__ float2 turn1(float x, float y, float2 cs) {
+    return make_float2(__fmaf_rn(x, cs.x, -__fmul_rn(y, cs.y)), __fmaf_rn(x, cs.y, __fmul_rn(y, cs.x)));
+}
+__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The two words of a pair's features (fp32), or of two pairs' (bf16).
+template <typename T>
+__device__ __forceinline__ void turn_halves(uint32_t& a, uint32_t& b, const float2* cs) {
+    if constexpr (sizeof(T) == 4) {
+        const float2 z = turn1(__uint_as_float(a), __uint_as_float(b), cs[0]);
+        a = __float_as_uint(z.x), b = __float_as_uint(z.y);
+    } else {
+        const float2 z = turn1(low_bf16(a), low_bf16(b), cs[0]), w = turn1(high_bf16(a), high_bf16(b), cs[1]);
+        a = pack_bf16(z.x, w.x), b = pack_bf16(z.y, w.y);
     }
-    const int off = turns ? e * N : plan.rot + (e - turned) * kTail;
-    const T* qi = static_cast<const T*>(q.in) + tok * q.in_stride + off;
-    const T* ki = static_cast<const T*>(k.in) + tok * k.in_stride + off;
-    T* qo = static_cast<T*>(q.out) + tok * q.out_stride + off;
-    T* ko = static_cast<T*>(k.out) + tok * k.out_stride + off;
-    auto in_at = [&](int h) { return h < q.heads ? qi + h * plan.d : ki + (h - q.heads) * plan.d; };
-    auto out_at = [&](int h) { return h < q.heads ? qo + h * plan.d : ko + (h - q.heads) * plan.d; };
-    for (int h1 = h0; h1 < heads; h1 += kInFlight * split) {
-        if (turns) {
-            V a[kInFlight], b[kInFlight];
+}
+template <typename T, bool kHalves>
+__device__ __forceinline__ void turn16(uint4& a, uint4& b, const float2* cs) {
+    if constexpr (kHalves) {
+        constexpr int n = 4 / (int)sizeof(T);
+        turn_halves<T>(a.x, b.x, cs);
+        turn_halves<T>(a.y, b.y, cs + n);
+        turn_halves<T>(a.z, b.z, cs + 2 * n);
+        turn_halves<T>(a.w, b.w, cs + 3 * n);
+    } else if constexpr (sizeof(T) == 4) {
+        turn_halves<T>(a.x, a.y, cs);
+        turn_halves<T>(a.z, a.w, cs + 1);
+    } else {
+        uint32_t* w[4] = {&a.x, &a.y, &a.z, &a.w};
 #pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const int h = h1 + u * split;
-                if (h < heads) {
-                    a[u] = *reinterpret_cast<const V*>(in_at(h));
-                    if constexpr (kHalves) b[u] = *reinterpret_cast<const V*>(in_at(h) + half);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const int h = h1 + u * split;
-                if (h < heads) {
-#pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        T& xt = kHalves ? a[u].v[j] : a[u].v[2 * j];
-                        T& yt = kHalves ? b[u].v[j] : a[u].v[2 * j + 1];
-                        const float x = to_f(xt), y = to_f(yt);
-                        xt = from_f<T>(x * c[j] - y * s[j]);
-                        yt = from_f<T>(x * s[j] + y * c[j]);
-                    }
-                    *reinterpret_cast<V*>(out_at(h)) = a[u];
-                    if constexpr (kHalves) *reinterpret_cast<V*>(out_at(h) + half) = b[u];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const int h = h1 + u * split;
-                if (h < heads) *reinterpret_cast<Tail*>(out_at(h)) = *reinterpret_cast<const Tail*>(in_at(h));
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 z = turn1(low_bf16(*w[i]), high_bf16(*w[i]), cs[i]);
+            *w[i] = pack_bf16(z.x, z.y);
         }
     }
 }
+// One pair in single elements.
+template <typename T, typename R>
+__device__ __forceinline__ void turn_single(R& a, R& b, float2 cs) {
+    if constexpr (sizeof(T) == 4) {
+        const float2 z = turn1(__uint_as_float(a), __uint_as_float(b), cs);
+        a = __float_as_uint(z.x), b = __float_as_uint(z.y);
+    } else {
+        const float2 z = turn1(low_bf16(a), low_bf16(b), cs);
+        const uint32_t w = pack_bf16(z.x, z.y);
+        a = (R)w, b = (R)(w >> 16);
+    }
+}
 
-template <typename T, bool kHalves, int NP>
+// An item is a place of up to `group` heads of q or of k, of one token.
+template <typename T, bool kHalves, bool kWide>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Plan plan, Side q, Side k,
+                                                          const int* __restrict__ positions, int tokens, int per_block,
+                                                          int group, float sign) {
+    using F = Form<T, kHalves, kWide>;
+    using R = typename RawOf<F::kBytes>::type;
+    extern __shared__ float2 cs[];  // [token][pair]
+    const int half = plan.rot >> 1, d = plan.d;
+    const int tok0 = blockIdx.x * per_block;
+    const int n_tok = min(per_block, tokens - tok0);
+    const int turned = half / F::NP;  // places that turn
+    const int per_head = turned + (d - plan.rot) / F::kTail;
+    const int q_groups = (q.heads + group - 1) / group, groups = q_groups + (k.heads + group - 1) / group;
+    const int items = n_tok * groups * per_head;
+    const int other = kHalves ? half : 1;  // from a pair's first feature to its second
+    int t = 0, e = 0, n = 0;
+    const T* in = nullptr;
+    T* out = nullptr;
+    R a[kInFlight], b[kInFlight];
+    auto open = [&](int i) {  // item i's place; its loads
+        const int tg = i / per_head;
+        e = i - tg * per_head;
+        t = tg / groups;
+        int gr = tg - t * groups;
+        const bool is_k = gr >= q_groups;
+        if (is_k) gr -= q_groups;
+        const Side& sd = is_k ? k : q;
+        const int h0 = gr * group;
+        n = min(group, sd.heads - h0);
+        const int off = h0 * d + (e < turned ? e * (kWide || kHalves ? F::kStep : 2) : plan.rot + (e - turned) * F::kTail);
+        in = static_cast<const T*>(sd.in) + (tok0 + t) * sd.in_stride + off;
+        out = static_cast<T*>(sd.out) + (tok0 + t) * sd.out_stride + off;
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u)
+            if (u < n) {
+                a[u] = *reinterpret_cast<const R*>(in + u * d);
+                if (F::kLoads == 2 && e < turned) b[u] = *reinterpret_cast<const R*>(in + u * d + other);
+            }
+    };
+    int i = threadIdx.x;
+    if (i < items) open(i);
+    for (int p = threadIdx.x; p < n_tok * half; p += kThreads) {
+        const int pt = p / half, pp = p - pt * half;
+        const long long pos = positions[(size_t)(tok0 + pt) * plan.axes + plan.axis[pp]];
+        const long long phase = (long long)((unsigned long long)pos * plan.freq[pp]);
+        float s, c;
+        sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
+        cs[p] = make_float2(c, s * sign);
+    }
+    __syncthreads();
+    for (; i < items; i += kThreads) {
+        if (i >= kThreads) open(i);
+        const bool turns = e < turned;
+        float2 c[F::NP];
+        if (turns) {
+#pragma unroll
+            for (int j = 0; j < F::NP; ++j) c[j] = cs[t * half + e * F::NP + j];
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u)
+            if (u < n) {
+                if (turns) {
+                    if constexpr (kWide)
+                        turn16<T, kHalves>(a[u], b[u], c);
+                    else
+                        turn_single<T>(a[u], b[u], c[0]);
+                    if (F::kLoads == 2) *reinterpret_cast<R*>(out + u * d + other) = b[u];
+                }
+                *reinterpret_cast<R*>(out + u * d) = a[u];
+            }
+    }
+}
+
+template <typename T, bool kHalves, bool kWide>
 cudaError_t launch_as(const Plan& p, const Side& q, const Side& k, const int* pos, int tokens, float sign,
                       cudaStream_t st) {
-    constexpr int kTail = NP == 1 ? 1 : kHalves ? NP : 2 * NP;
-    const long long places = (long long)tokens * (p.rot / 2 / NP + (p.d - p.rot) / kTail);
-    const int heads = q.heads + k.heads;
-    // Threads per place: one while that fills the GPU (1000 threads per SM);
-    // with fewer tokens each thread takes fewer heads, down to one
-    long long split = (148 * 1000 + places - 1) / places;
-    if (split > heads) split = heads;
-    const long long blocks = (places * split + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    rotary_kernel<T, kHalves, NP><<<(unsigned)blocks, kThreads, 0, st>>>(p, q, k, pos, tokens, (int)split, sign);
+    using F = Form<T, kHalves, kWide>;
+    const int per_head = p.rot / 2 / F::NP + (p.d - p.rot) / F::kTail;
+    // Heads of an item: as many as are in flight, fewer when there are few
+    // tokens (a token's heads then spread over the block's threads); tokens of
+    // a block: what its threads have one item each for
+    int group = kInFlight, groups;
+    while (true) {
+        groups = (q.heads + group - 1) / group + (k.heads + group - 1) / group;
+        if (group == 1 || (long long)tokens * per_head * groups >= 148 * 512) break;
+        group /= 2;
+    }
+    int per_block = kThreads / (per_head * groups);
+    per_block = per_block < 1 ? 1 : per_block > kMaxTokensPerBlock ? kMaxTokensPerBlock : per_block;
+    const int grid = (tokens + per_block - 1) / per_block;
+    rotary_kernel<T, kHalves, kWide>
+        <<<grid, kThreads, (size_t)per_block * (p.rot / 2) * sizeof(float2), st>>>(p, q, k, pos, tokens, per_block, group, sign);
     return cudaGetLastError();
 }
 
 template <typename T, bool kHalves>
 cudaError_t launch(const Plan& p, const Side& q, const Side& k, const int* pos, int tokens, float sign, bool wide,
                    cudaStream_t st) {
-    constexpr int kWide = (kHalves ? 16 : 8) / (int)sizeof(T);  // pairs per 16-byte vector
-    return wide ? launch_as<T, kHalves, kWide>(p, q, k, pos, tokens, sign, st)
-                : launch_as<T, kHalves, 1>(p, q, k, pos, tokens, sign, st);
+    return wide ? launch_as<T, kHalves, true>(p, q, k, pos, tokens, sign, st)
+                : launch_as<T, kHalves, false>(p, q, k, pos, tokens, sign, st);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
