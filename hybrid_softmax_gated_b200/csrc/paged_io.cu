@@ -81,11 +81,23 @@ __device__ __forceinline__ Share share_of(int rows, int per_warp) {
     return Share{(int)tok, (int)(w - tok * parts) * per_warp};
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 template <typename T>
 struct Lane16;  // elements of 16 bytes
 template <>
 struct Lane16<__nv_bfloat16> {
     static constexpr int n = 8;
+    // largest magnitude of the 16 bytes, NaN if one is
+    static __device__ __forceinline__ float amax(const uint4& u) {
+        auto b = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(b(u.x), b(u.y)), __hmax2_nan(b(u.z), b(u.w)));
+        return __bfloat162float(__hmax_nan(m.x, m.y));
+    }
     static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -107,6 +119,11 @@ struct Lane16<__nv_bfloat16> {
 template <>
 struct Lane16<float> {
     static constexpr int n = 4;
+    static __device__ __forceinline__ float amax(const uint4& u) {
+        float x[4];
+        unpack(u, x);
+        return max_nan(max_nan(fabsf(x[0]), fabsf(x[1])), max_nan(fabsf(x[2]), fabsf(x[3])));
+    }
     static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
         x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y);
         x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
@@ -151,6 +168,21 @@ __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool 
         }
         const Place pl = find_place(g, b, nullptr, false, sh.tok, err);
         if (pl.page < 0) return;
+        // The scales of the rows, the two divisions of each in one lane only
+        float scale = 0.f, inverse = 0.f;
+        if constexpr (kCodes) {
+            float mine = 0.f;
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                float m = Lane16<T>::amax(raw[u]);
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                mine = c == u ? m : mine;
+            }
+            const bool finite = mine < INFINITY;
+            scale = scale_of(mine, finite);
+            inverse = finite ? 1.f / scale : 0.f;
+        }
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
             const int r = sh.r0 + u * kPer + sub;
@@ -160,22 +192,11 @@ __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool 
             if constexpr (!kCodes) {
                 if (on) reinterpret_cast<uint4*>(dst)[row * kLanes + c] = raw[u];
             } else {
-                float x[n];
-                Lane16<T>::unpack(raw[u], x);
-                float amax = 0.f;
-                bool finite = true;
-#pragma unroll
-                for (int i = 0; i < n; ++i) {
-                    amax = fmaxf(amax, fabsf(x[i]));
-                    finite = finite && fabsf(x[i]) < INFINITY;
-                }
-                if (!finite) amax = INFINITY;
-#pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                finite = amax < INFINITY;
-                const float s = scale_of(amax, finite);
-                const float inv = finite ? 1.f / s : 0.f;
+                const float s = __shfl_sync(0xffffffffu, scale, u, kLanes);
+                const float inv = __shfl_sync(0xffffffffu, inverse, u, kLanes);
                 if (on) {
+                    float x[n];
+                    Lane16<T>::unpack(raw[u], x);
                     uint32_t w[n / 4];
 #pragma unroll
                     for (int i = 0; i < n / 4; ++i) {
@@ -185,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool 
                             const float2 y = make_float2(x[4 * i + j] * inv, x[4 * i + j + 1] * inv);
                             code |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (8 * j);
                         }
-                        w[i] = finite ? code : 0u;
+                        w[i] = inv != 0.f ? code : 0u;  // (a row that is not finite)
                     }
                     uint32_t* to = reinterpret_cast<uint32_t*>(dst) + (row * kLanes + c) * (n / 4);
                     if constexpr (n == 8)
