@@ -27,7 +27,7 @@
 // element.  e4m3 products run at twice the rate of bf16 ones, so two terms cost
 // what one bf16 product does, and K needs no conversion.  P has no such split
 // (its small weights would need bf16's exponents): V's codes become bf16 tiles,
-// exactly, in warps 12-15, which also split Q.  The keys' scales multiply their
+// exactly, in warps 2 and 3, which also split Q.  The keys' scales multiply their
 // scores and the values' scales the weights, in fp32.
 //
 // Softmax statistics, sums and accumulators are fp32.  The weights are
@@ -61,22 +61,20 @@ constexpr int kRows = 128;  // rows of a half tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S/P buffers at 0, 128; O_0, O_1 at 256, 384
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kConvWarps = 4;
+constexpr int kThreads = 384;
+constexpr int kConvWarps = 2;
+// Registers per thread at launch (one CTA per SM) and after the split: warps
+// 0-3 hand theirs to the two softmax warpgroups.
+constexpr int kRegsLaunch = 168, kRegsLow = 96, kRegsHigh = 200;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
 constexpr int kMinUnits = 2;
 
 template <bool kCodes>
 struct Cfg {
-    static constexpr int kThreads = kCodes ? 512 : 384;
     static constexpr int kK = kCodes ? 3 : 2;       // K tiles in their ring
     static constexpr int kKBytes = kCodes ? kCodeTile : (int)kTileBytes;
     static constexpr int kV = 2;                    // V tiles (bf16) in theirs
     static constexpr int kStaged = 2;               // blocks of V's codes on their way
-    // Registers per thread at launch (one CTA per SM) and after the split:
-    // the other warpgroups hand theirs to the two softmax warpgroups.
-    static constexpr int kRegsLaunch = kCodes ? 128 : 168;
-    static constexpr int kRegsLow = kCodes ? 72 : 96, kRegsConv = 72, kRegsHigh = kCodes ? 184 : 200;
-    static_assert(128 * kRegsLow + 256 * kRegsHigh + (kCodes ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch,
-                  "register split");
 };
 
 template <bool kCodes>
@@ -153,7 +151,7 @@ __device__ __forceinline__ RowOf row_of(const Desc& d, int row, int wg, int G, i
 }
 
 template <bool kCodes>
-__global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttend a,
                     float scale_log2) {
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
         return true;
     };
 
-    if (warp < 4) ptx::setmaxnreg_dec<C::kRegsLow>();
+    if (warp < 4) ptx::setmaxnreg_dec<kRegsLow>();
     if (warp == 0) {
         // ------------------------------------------------------ loader --
         if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, TQ, HT, wwait)) fail();
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             ptx::umma_commit_w(ptx::smem_u32(&sm.drain));
             ptx::mbar_wait_bounded(ptx::smem_u32(&sm.drain), 0, &no_abort, kWaitLimitNs);
         }
-    } else if (warp == 3) {
+    } else if (!kCodes && warp == 3) {
         // ----------------------------------- slots behind the last key --
         if constexpr (!kCodes) {
             int vn = 0, tails = 0;
@@ -346,11 +344,10 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
             }
             if (!ok) fail();
         }
-    } else if (warp >= 12) {
+    } else if (kCodes && warp < 4) {
         // ----------------- Q in two terms, V's codes -> bf16 tiles --
         if constexpr (kCodes) {
-            ptx::setmaxnreg_dec<C::kRegsConv>();
-            const int cw = warp - 12;
+            const int cw = warp - 2;
             int vn = 0, qn = 0;
             bool ok = true;
             for (int si = 0; ok; ++si) {
@@ -378,21 +375,27 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                     // lanes of a quarter warp take eight rows: loads and stores
                     // of the swizzled tiles then touch every bank once
                     const int r7 = lane & 7, c = lane >> 3;
-                    const uint8_t* from = sm.st[s] + (cw * 32 + r7) * 128 + ((c ^ r7) << 4);
-                    const uint32_t to = ptx::smem_u32(sm.v[s]) + (uint32_t)((cw * 32 + r7) * 128 + (((2 * c) ^ r7) << 4));
+                    const uint8_t* from = sm.st[s] + (cw * 64 + r7) * 128 + ((c ^ r7) << 4);
+                    const uint32_t to = ptx::smem_u32(sm.v[s]) + (uint32_t)((cw * 64 + r7) * 128 + (((2 * c) ^ r7) << 4));
                     const uint32_t to2 = to ^ 16u;
-                    const uint8_t* from2 = sm.st[s] + (cw * 32 + r7) * 128 + (((c + 4) ^ r7) << 4);
+                    const uint8_t* from2 = sm.st[s] + (cw * 64 + r7) * 128 + (((c + 4) ^ r7) << 4);
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 16; i0 += 4) {
+                        uint4 u[4];  // 16 codes each: features 64 half + 16 c ..., of rows 8 apart
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int half = i & 1, row8 = (i >> 1) * 1024;  // 16 codes: features 64 half + 16 c ..., 8 rows on
-                        const uint4 u = *reinterpret_cast<const uint4*>((half ? from2 : from) + row8);
-                        uint32_t y[8];
-                        codes_to_bf16(u.x, y[0], y[1]);
-                        codes_to_bf16(u.y, y[2], y[3]);
-                        codes_to_bf16(u.z, y[4], y[5]);
-                        codes_to_bf16(u.w, y[6], y[7]);
-                        ptx::st_shared_v4(to + half * kHalfBytes + row8, y[0], y[1], y[2], y[3]);
-                        ptx::st_shared_v4(to2 + half * kHalfBytes + row8, y[4], y[5], y[6], y[7]);
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = *reinterpret_cast<const uint4*>((i & 1 ? from2 : from) + ((i0 + i) >> 1) * 1024);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t y[8];
+                            codes_to_bf16(u[i].x, y[0], y[1]);
+                            codes_to_bf16(u[i].y, y[2], y[3]);
+                            codes_to_bf16(u[i].z, y[4], y[5]);
+                            codes_to_bf16(u[i].w, y[6], y[7]);
+                            const uint32_t at = (i & 1) * kHalfBytes + ((i0 + i) >> 1) * 1024;
+                            ptx::st_shared_v4(to + at, y[0], y[1], y[2], y[3]);
+                            ptx::st_shared_v4(to2 + at, y[4], y[5], y[6], y[7]);
+                        }
                     }
                     ptx::fence_proxy_async_smem();
                     arrive1(&sm.v_full[s]);
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
         }
     } else if (warp >= 4) {
         // ------------------------------------------ softmax, epilogue --
-        ptx::setmaxnreg_inc<C::kRegsHigh>();
+        ptx::setmaxnreg_inc<kRegsHigh>();
         const int wg = (warp - 4) >> 2;                // S/P buffer and accumulator
         const int row = ((warp & 3) << 5) + lane;      // row of the half tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -531,6 +534,7 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 // buffer (behind the scores that are still to be loaded again)
                 auto weigh = [&](const uint32_t(&y)[32], int c) {
                     uint32_t pk[16];
+                    float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 xi = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
@@ -541,8 +545,8 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                         sum4[i & 3] = ptx::add2(sum4[i & 3], p);
                         if constexpr (kCodes) {
                             // (a hidden value's scale may be anything)
-                            const float2 v2 = *reinterpret_cast<const float2*>(vscale + 32 * c + 2 * i);
-                            float2 w = ptx::mul2(p, v2);
+                            if (i % 2 == 0) v4 = *reinterpret_cast<const float4*>(vscale + 32 * c + 2 * i);
+                            float2 w = ptx::mul2(p, i % 2 == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
                             if (masked) {
                                 w.x = p.x == 0.f ? 0.f : w.x;
                                 w.y = p.y == 0.f ? 0.f : w.y;
@@ -715,40 +719,42 @@ __global__ void __launch_bounds__(Cfg<kCodes>::kThreads, 1)
                 __threadfence();
                 const float2* ml = a.work.ml + half * kRows + row;
                 auto slot_of = [&](int c) { return (size_t)paged::partial_slot(sm.pl, c, d.base); };
-                float mm = -INFINITY, ll = 0.f;
+                float mm = -INFINITY;
+#pragma unroll 4
                 for (int c = d.c0; c <= d.c1; ++c) mm = fmaxf(mm, __ldcg(ml + slot_of(c) * 2 * kRows).x);
-                for (int c = d.c0; c <= d.c1; ++c) {
-                    const float2 x = __ldcg(ml + slot_of(c) * 2 * kRows);
-                    ll += x.x == -INFINITY ? x.y : x.y * ptx::ex2(x.x - mm);
-                }
-                const float inv_l = ll == 0.f ? 0.f : 1.f / ll;
                 const float4* po = reinterpret_cast<const float4*>(a.work.o) + (size_t)half * 32 * kRows +
                                    (size_t)(col0 / 4) * kRows + row;
+                // 64 columns a time, a piece's loads all in flight together
 #pragma unroll 1
-                for (int c8 = 0; c8 < chunks; ++c8) {
-                    float acc[32];
+                for (int c16 = 0; c16 < chunks / 2; ++c16) {
+                    float acc[64], ll = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+                    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+#pragma unroll 1
                     for (int c = d.c0; c <= d.c1; ++c) {
-                        const float mc = __ldcg(ml + slot_of(c) * 2 * kRows).x;
-                        const float w = mc == -INFINITY ? 1.f : ptx::ex2(mc - mm);
-                        const float4* from = po + slot_of(c) * 2 * 32 * kRows + (size_t)(8 * c8) * kRows;
+                        const float2 x = __ldcg(ml + slot_of(c) * 2 * kRows);
+                        const float4* from = po + slot_of(c) * 2 * 32 * kRows + (size_t)(16 * c16) * kRows;
+                        float4 y[16];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 x = __ldcg(from + (size_t)i * kRows);
-                            acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
-                            acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
-                            acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
-                            acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+                        for (int i = 0; i < 16; ++i) y[i] = __ldcg(from + (size_t)i * kRows);
+                        const float w = x.x == -INFINITY ? 1.f : ptx::ex2(x.x - mm);
+                        ll = fmaf(w, x.y, ll);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            acc[4 * i] = fmaf(w, y[i].x, acc[4 * i]);
+                            acc[4 * i + 1] = fmaf(w, y[i].y, acc[4 * i + 1]);
+                            acc[4 * i + 2] = fmaf(w, y[i].z, acc[4 * i + 2]);
+                            acc[4 * i + 3] = fmaf(w, y[i].w, acc[4 * i + 3]);
                         }
                     }
+                    const float inv_l = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w[e] = ptx::pack_bf16x2(acc[8 * i + 2 * e] * inv_l, acc[8 * i + 2 * e + 1] * inv_l);
-                        *reinterpret_cast<uint4*>(out + col0 + 32 * c8 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(out + col0 + 64 * c16 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
@@ -776,7 +782,7 @@ bool ready() {
     }
     // the warpgroups' register split needs the launch count it was sized for
     cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != Cfg<kCodes>::kRegsLaunch) {
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kRegsLaunch) {
         cudaGetLastError();
         return false;
     }
@@ -799,7 +805,7 @@ cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int grid = max_ctas > 0 && max_ctas < sms ? max_ctas : sms;
     static_assert(2 * 2 * kRows <= kPagedRowsPerSm, "workspace rows");
-    paged_tc_kernel<kCodes><<<grid, Cfg<kCodes>::kThreads, sizeof(Smem<kCodes>), st>>>(
+    paged_tc_kernel<kCodes><<<grid, kThreads, sizeof(Smem<kCodes>), st>>>(
         q, k, v, a, a.scale * 1.4426950408889634f);
     return cudaGetLastError();
 }

@@ -104,40 +104,50 @@ __device__ __forceinline__ void clear_tail(uint8_t* tile, int halves, int key0, 
 template <uint32_t kHalf>
 __device__ __forceinline__ void split_q(uint8_t* tile, float* row_scale, int rows, int w, int warps, float scale) {
     const int lane = threadIdx.x & 31, c = lane & 15;
-    for (int r0 = w * 2; r0 < rows; r0 += 2 * warps) {
-        const int r = r0 + (lane >> 4);
-        const uint4 u = *reinterpret_cast<const uint4*>(tile + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
-        float x[8], amax = 0.f;
-        bool finite = true;
+    constexpr int kBatch = 4;  // rows a lane has in flight
+    for (int base = w * 2; base < rows; base += 2 * kBatch * warps) {
+        uint4 u[kBatch];
+        float amax[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = __uint_as_float(i & 1 ? u4[i >> 1] & 0xffff0000u : u4[i >> 1] << 16);
-            amax = fmaxf(amax, fabsf(x[i]));
-            finite = finite && fabsf(x[i]) < INFINITY;
+        for (int t = 0; t < kBatch; ++t) {
+            const int r = base + 2 * warps * t + (lane >> 4);
+            u[t] = make_uint4(0u, 0u, 0u, 0u);
+            if (base + 2 * warps * t < rows)
+                u[t] = *reinterpret_cast<const uint4*>(tile + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            auto mag = [](uint32_t x) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)); };
+            const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(mag(u[t].x), mag(u[t].y)), __hmax2_nan(mag(u[t].z), mag(u[t].w)));
+            const float f = __bfloat162float(__hmax_nan(m.x, m.y));
+            amax[t] = f < INFINITY ? f : INFINITY;  // (NaN: infinity, too)
         }
-        if (!finite) amax = INFINITY;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // (every lane has read the row: it may be overwritten)
-        int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);  // amax 2^k in [2^7, 2^8)
-        k = k > 120 ? 120 : k;
-        const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
-        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+        for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float2 y = make_float2(x[i] * up, x[i + 1] * up);
-            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-            const __nv_fp8x2_storage_t l =
-                __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
-            hi[i >> 2] |= (uint32_t)h << (8 * (i & 2));
-            lo[i >> 2] |= (uint32_t)l << (8 * (i & 2));
+            for (int t = 0; t < kBatch; ++t) amax[t] = fmaxf(amax[t], __shfl_xor_sync(0xffffffffu, amax[t], o));
+        // (every lane has read its part of these rows: they may be overwritten)
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+            const int r = base + 2 * warps * t + (lane >> 4);
+            if (base + 2 * warps * t >= rows) continue;
+            int k = 7 - ((int)(__float_as_uint(amax[t]) >> 23) - 127);  // amax 2^k in [2^7, 2^8)
+            k = k > 120 ? 120 : k;
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
+            const uint32_t words[4] = {u[t].x, u[t].y, u[t].z, u[t].w};
+            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 y = make_float2(__uint_as_float(words[i] << 16) * up, __uint_as_float(words[i] & 0xffff0000u) * up);
+                const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+                const __nv_fp8x2_storage_t l =
+                    __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+                hi[i >> 1] |= (uint32_t)h << (16 * (i & 1));
+                lo[i >> 1] |= (uint32_t)l << (16 * (i & 1));
+            }
+            uint8_t* to = tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + kHalf) = make_uint2(lo[0], lo[1]);
+            if (c == 0) row_scale[r] = amax[t] < INFINITY ? down * scale : __int_as_float(0x7fffffff);
         }
-        uint8_t* to = tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(to + kHalf) = make_uint2(lo[0], lo[1]);
-        if (c == 0) row_scale[r] = amax < INFINITY ? down * scale : __int_as_float(0x7fffffff);
     }
 }
 
