@@ -85,14 +85,13 @@ __device__ __forceinline__ Blocks blocks_of(const PagedMask& m, const Seq& q, in
 }
 
 // ---- schedule ---------------------------------------------------------------
-// A tile is up to TQ new tokens of one sequence with the G query heads of one
-// key head; a unit is one tile, or one half of a tile of two (HT: tokens of a
-// half; HT = TQ: no halves), against one block of KB keys (a tile that sees
-// nothing still counts: its zeros are written).  In the order (head,
-// sequence, tile, block), CTA c takes the units [c U / P, (c + 1) U / P) of
-// all U, P CTAs taking part.  A tile cut by such a border leaves one partial
-// in each CTA's piece of it; the last CTA to arrive merges them, in order.
-// Nobody waits for anybody.
+// A tile is a run of new tokens of one sequence with the G query heads of one
+// key head; it counts some units (its cost) for each block of KB keys that it
+// sees and some for itself.  In the order (head, sequence, tile, block), CTA c
+// takes the units [c U / P, (c + 1) U / P) of all U, P CTAs taking part; a
+// border in a small tile, or in what a tile costs for itself, moves back to the
+// tile's start.  A tile cut by a border leaves one partial in each CTA's piece
+// of it; the last CTA to arrive merges them, in order.  Nobody waits for anybody.
 // Every CTA works this out from the device's tables: no host copy of the
 // lengths, no planning launch.
 struct PlanSmem {
@@ -101,6 +100,7 @@ struct PlanSmem {
     long long warp_sum[32];
     long long start_base;          // units of the head before the first tile
     int start_seq, start_tile;
+    long long start, end;          // the CTA's first unit and its last + 1, of their heads
 };
 
 struct Cursor {
@@ -140,22 +140,35 @@ __device__ __forceinline__ Seq seq_of(const PlanSmem& ps, int s) {
     return ps.total[s] < 0 ? Seq{0, 0, 0} : Seq{ps.q_off[s], ps.q_off[s + 1] - ps.q_off[s], ps.total[s]};
 }
 
-// Units of a tile's block: 2 if the tile has more tokens than one half of it
-// holds (both halves work on every block), else 1.
-__device__ __forceinline__ int weight_of(const Seq& q, int t, int TQ, int HT) { return q.n - t * TQ > HT ? 2 : 1; }
+// Tiles of a kernel: tokens of a tile and of one half of it (half = tokens: no
+// halves); in units, what a block of keys costs a tile of two halves, one whose
+// tokens fit a half and one whose tokens fit a quarter, what a tile costs on
+// top (its queries, its outputs), and up to how many it is never cut.
+struct Tiling {
+    int tokens, half, pair_cost, single_cost, small_cost, tile_cost, whole;
+};
+__device__ __forceinline__ int weight_of(const Seq& q, int t, const Tiling& tl) {
+    const int n = q.n - t * tl.tokens;
+    return n > tl.half ? tl.pair_cost : 2 * n > tl.half ? tl.single_cost : tl.small_cost;
+}
 
 template <int KB>
-__device__ __forceinline__ int units_of(const PagedMask& m, const Seq& q, int t, int TQ, int HT) {
-    const int i0 = t * TQ;
-    const int c = blocks_of<KB>(m, q, i0, q.n - i0 < TQ ? q.n - i0 : TQ).count();
-    return (c > 0 ? c : 1) * weight_of(q, t, TQ, HT);
+__device__ __forceinline__ int units_of(const PagedMask& m, const Seq& q, int t, const Tiling& tl) {
+    const int i0 = t * tl.tokens;
+    const int c = blocks_of<KB>(m, q, i0, q.n - i0 < tl.tokens ? q.n - i0 : tl.tokens).count();
+    return (c > 0 ? c : 1) * weight_of(q, t, tl) + tl.tile_cost;
 }
 
 // The whole block.  tiles: kPagedMaxSeqs + 1 integers of shared memory for the
 // exclusive prefix of the sequences' tiles, free again afterwards.  grid CTAs; no CTA gets fewer than min_units units while
 // others have them (each cut costs a partial and its merge).
+// Where a border at unit u of a tile [at, at + units) goes.
+__device__ __forceinline__ long long border(long long u, long long at, int units, const Tiling& tl) {
+    return units <= tl.whole || u - at <= tl.tile_cost ? at : u;
+}
+
 template <int KB>
-__device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMask& m, int TQ, int HT,
+__device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMask& m, const Tiling& tl,
                           int min_units, PlanSmem& ps, int* tiles, int* err) {
     const int N = blockDim.x, tid = threadIdx.x;
     // tiles of each sequence
@@ -167,7 +180,7 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
         ps.q_off[s] = b.q_off[s];
         ps.total[s] = q.n > 0 ? q.total : -1;  // (-1: no rows, or wrong entries)
         tiles[s] = mine;
-        mine += (q.n + TQ - 1) / TQ;
+        mine += (q.n + tl.tokens - 1) / tl.tokens;
     }
     if (tid == 0) ps.q_off[b.S] = b.q_off[b.S];
     long long all;
@@ -196,33 +209,38 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
     long long sum = 0;
     for (int f = f0, s = s_first; f < f1; ++f) {
         while (f >= tiles[s + 1]) ++s;
-        sum += units_of<KB>(m, seq_of(ps, s), f - tiles[s], TQ, HT);
+        sum += units_of<KB>(m, seq_of(ps, s), f - tiles[s], tl);
     }
     const long long pre = block_prefix(sum, ps, &all);
     pl.U = all * g.Hk;
     pl.P = gridDim.x;
-    if (pl.U < (long long)pl.P * min_units) pl.P = (int)((pl.U + min_units - 1) / min_units);
+    if (pl.U < (long long)pl.P * min_units) pl.P = pl.U < min_units ? 1 : (int)(pl.U / min_units);
     if ((int)blockIdx.x >= pl.P) return pl;
     pl.u0 = pl.U * blockIdx.x / pl.P;
     pl.u1 = pl.U * (blockIdx.x + 1) / pl.P;
-    const int h = (int)(pl.u0 / all);
-    const long long rem = pl.u0 - h * all;
-    if (sum > 0 && rem >= pre && rem < pre + sum) {
+    // the tiles under both borders
+    const int h0 = (int)(pl.u0 / all), h1 = (int)(pl.u1 / all);
+    const long long rem0 = pl.u0 - h0 * all, rem1 = pl.u1 - h1 * all;
+    const bool has0 = rem0 >= pre && rem0 < pre + sum, has1 = rem1 >= pre && rem1 < pre + sum && rem1 > 0;
+    if (has0 || has1) {
         long long at = pre;
         for (int f = f0, s = s_first; f < f1; ++f) {
             while (f >= tiles[s + 1]) ++s;
-            const int u = units_of<KB>(m, seq_of(ps, s), f - tiles[s], TQ, HT);
-            if (rem < at + u) {
+            const int u = units_of<KB>(m, seq_of(ps, s), f - tiles[s], tl);
+            if (has0 && rem0 >= at && rem0 < at + u) {
                 ps.start_base = at;
                 ps.start_seq = s;
                 ps.start_tile = f - tiles[s];
-                break;
+                ps.start = border(rem0, at, u, tl);
             }
+            if (has1 && rem1 >= at && rem1 < at + u) ps.end = border(rem1, at, u, tl);
             at += u;
         }
     }
     __syncthreads();
-    pl.first = Cursor{h, ps.start_seq, ps.start_tile, h * all + ps.start_base};
+    pl.first = Cursor{h0, ps.start_seq, ps.start_tile, h0 * all + ps.start_base};
+    pl.u0 = h0 * all + ps.start;
+    if (rem1 > 0) pl.u1 = h1 * all + ps.end;
     return pl;
 }
 
@@ -237,36 +255,36 @@ struct Piece {
 };
 template <int KB>
 __device__ __forceinline__ Piece piece_at(const PagedMask& m, const PlanSmem& ps, const Plan& pl, const Cursor& c,
-                                          int TQ, int HT) {
+                                          const Tiling& tl) {
     Piece p;
     p.q = seq_of(ps, c.s);
-    p.i0 = c.t * TQ;
-    p.n = min(TQ, p.q.n - p.i0);
+    p.i0 = c.t * tl.tokens;
+    p.n = min(tl.tokens, p.q.n - p.i0);
     p.blocks = blocks_of<KB>(m, p.q, p.i0, p.n);
     const int count = p.blocks.count();
-    const int w = weight_of(p.q, c.t, TQ, HT);
-    p.units = (count > 0 ? count : 1) * w;
+    const int w = weight_of(p.q, c.t, tl);
+    p.units = (count > 0 ? count : 1) * w + tl.tile_cost;
     const long long a = pl.u0 > c.base ? pl.u0 - c.base : 0;
     const long long z = pl.u1 - c.base < p.units ? pl.u1 - c.base : p.units;
-    // (a border inside a block of two units leaves the block to the CTA that
-    // has its first one)
-    p.b0 = count > 0 ? (int)(a + w - 1) / w : 0;
-    p.b1 = count > 0 ? (int)(z + w - 1) / w : 0;
+    // (a border inside a block leaves it to the CTA that has its first unit)
+    p.b0 = count > 0 && a > 0 ? ((int)a - tl.tile_cost + w - 1) / w : 0;
+    p.b1 = count > 0 ? ((int)z - tl.tile_cost + w - 1) / w : 0;
     if (a == 0 && z == p.units) {
         p.c0 = p.c1 = blockIdx.x;
     } else {
         p.c0 = (int)(((c.base + 1) * pl.P - 1) / pl.U);
+        if (pl.U * (p.c0 + 1) / pl.P - c.base <= tl.tile_cost) ++p.c0;  // (that border moved to the tile's start)
         p.c1 = (int)(((c.base + p.units) * pl.P - 1) / pl.U);
     }
     return p;
 }
 // To the next tile; false when it is not this CTA's.
-__device__ __forceinline__ bool advance(const PlanSmem& ps, const Plan& pl, const PagedSeqs& b, int TQ, int units,
+__device__ __forceinline__ bool advance(const PlanSmem& ps, const Plan& pl, const PagedSeqs& b, const Tiling& tl, int units,
                                         Cursor& c) {
     c.base += units;
     if (c.base >= pl.u1) return false;
     ++c.t;
-    if (c.t * TQ >= seq_of(ps, c.s).n) {
+    if (c.t * tl.tokens >= seq_of(ps, c.s).n) {
         c.t = 0;
         do {
             if (++c.s == b.S) {

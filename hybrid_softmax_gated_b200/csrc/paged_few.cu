@@ -47,7 +47,10 @@ using paged::kWgWarps;
 
 constexpr int kThreads = 384;
 constexpr int kN = 16;                    // columns of a term (query rows)
-constexpr int kMinUnits = 2;
+// For the schedule, in blocks: what a tile costs on top of its blocks, up to
+// what it is not cut, and how much a CTA has at least.
+constexpr int kTileCost = 4, kWhole = 8, kMinUnits = 6;
+static_assert(kMinUnits > kTileCost, "one border at most in what a tile costs for itself");
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColS = 0, kColO = 128;  // four S buffers of 32 columns; O_0, O_1 of 64
 constexpr float kTopBits = 7.f;           // codes: the largest weight is 2^7 when c is set ...
@@ -163,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
-    const int TQ = NR / g.G;  // tokens of a tile
-    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, TQ, kMinUnits, sm.plan, sm.scratch, a.err);
+    const paged::Tiling tl{NR / g.G, NR / g.G, 1, 1, 1, kTileCost, kWhole};
+    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, tl, kMinUnits, sm.plan, sm.scratch, a.err);
     if (threadIdx.x == 0) sm.pl = pl;
     ptx::tc_fence_before();
     __syncthreads();
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ loader --
-        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, TQ, TQ, wwait)) fail();
+        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, tl, wwait)) fail();
     } else if (warp == 1) {
         // ------------------------------------------------------ issuer --
         // A: K (K-major) or V (MN-major), 128 rows; B: Q or P (K-major), 16 rows a term

@@ -47,15 +47,15 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
     Smem<RM>& sm = *reinterpret_cast<Smem<RM>*>(smem_raw);
     const PagedGeom& g = a.g;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const int TQ = R / g.G;
-    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, TQ, 1, sm.plan, sm.tiles, a.err);
+    const paged::Tiling tl{R / g.G, R / g.G, 1, 1, 1, 0, 1};
+    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, tl, 1, sm.plan, sm.tiles, a.err);
     if (pl.u1 == pl.u0) return;
     const T* q = static_cast<const T*>(a.q);
     const C* kp = static_cast<const C*>(a.pool.k);
     const C* vp = static_cast<const C*>(a.pool.v);
     paged::Cursor cur = pl.first;
     while (true) {
-        const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, TQ, TQ);
+        const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, tl);
         const int rows = pc.n * g.G;
         __syncthreads();  // the previous tile is done with shared memory
         for (int i = tid; i < R * 128; i += kThreads) {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
                 }
             }
         }
-        if (!paged::advance(sm.plan, pl, a.seqs, TQ, pc.units, cur)) break;
+        if (!paged::advance(sm.plan, pl, a.seqs, tl, pc.units, cur)) break;
     }
 }
 

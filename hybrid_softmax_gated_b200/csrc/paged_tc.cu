@@ -67,7 +67,11 @@ constexpr int kConvWarps = 2;
 // 0-3 hand theirs to the two softmax warpgroups.
 constexpr int kRegsLaunch = 168, kRegsLow = 96, kRegsHigh = 200;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
-constexpr int kMinUnits = 2;
+// For the schedule, in quarters of a block of two halves: the cost of a block,
+// of a tile on top of its blocks, up to what a tile is not cut, and how much a
+// CTA has at least.
+constexpr int kPairCost = 4, kSingleCost = 3, kSmallCost = 2, kTileCost = 6, kWhole = 16, kMinUnits = 8;
+static_assert(kMinUnits > kTileCost, "one border at most in what a tile costs for itself");
 
 template <bool kCodes>
 struct Cfg {
@@ -110,6 +114,7 @@ struct __align__(1024) Smem {
     uint64_t v_tail;             // a ragged block of V has landed, its tail not cleared yet
     uint64_t s_full[2];          // S of warpgroup w's item is in TMEM
     uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the last / first 64 keys written
+    uint64_t pv_half[2];         // an item's first half of P V is in O_w
     uint64_t pv_done[2];         // the piece's last P V of warpgroup w
     uint64_t o_free;             // 8 warp arrivals per piece: O_0, O_1 read out
     uint64_t ebar;               // 8 warp arrivals: the softmax warps meet
@@ -134,6 +139,37 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
     constexpr uint32_t k2p120 = 0x7b807b80u;  // 2^120 twice
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(k2p120));
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(k2p120));
+}
+
+// A staged block of V's codes -> a bf16 tile; warp ww of two does rows 64 ww ..
+__device__ __forceinline__ void convert_v(const uint8_t* st, uint32_t v, int ww) {
+    const int lane = threadIdx.x & 31;
+    // lanes of a quarter warp take eight rows: loads and stores
+    // of the swizzled tiles then touch every bank once
+    const int r7 = lane & 7, c = lane >> 3;
+    const uint8_t* from = st + (ww * 64 + r7) * 128 + ((c ^ r7) << 4);
+    const uint32_t to = v + (uint32_t)((ww * 64 + r7) * 128 + (((2 * c) ^ r7) << 4));
+    const uint32_t to2 = to ^ 16u;
+    const uint8_t* from2 = st + (ww * 64 + r7) * 128 + (((c + 4) ^ r7) << 4);
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += 4) {
+        uint4 u[4];  // 16 codes each: features 64 half + 16 c ..., of rows 8 apart
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = *reinterpret_cast<const uint4*>((i & 1 ? from2 : from) + ((i0 + i) >> 1) * 1024);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t y[8];
+            codes_to_bf16(u[i].x, y[0], y[1]);
+            codes_to_bf16(u[i].y, y[2], y[3]);
+            codes_to_bf16(u[i].z, y[4], y[5]);
+            codes_to_bf16(u[i].w, y[6], y[7]);
+            const uint32_t at = (i & 1) * kHalfBytes + ((i0 + i) >> 1) * 1024;
+            ptx::st_shared_v4(to + at, y[0], y[1], y[2], y[3]);
+            ptx::st_shared_v4(to2 + at, y[4], y[5], y[6], y[7]);
+        }
+    }
+    ptx::fence_proxy_async_smem();
 }
 
 // Row `row` of warpgroup wg's half tile: token of the tile and query head.
@@ -188,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             init(&sm.s_full[i], 1);
             init(&sm.p_half[i], kWgWarps);
             init(&sm.p_full[i], kWgWarps);
+            init(&sm.pv_half[i], 1);
             init(&sm.pv_done[i], 1);
         }
         init(&sm.v_tail, 1);
@@ -203,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
-    const int HT = kRows / g.G, TQ = 2 * HT;  // tokens of a half tile, of a tile
-    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, TQ, HT, kMinUnits, sm.plan, sm.scratch, a.err);
+    const int HT = kRows / g.G;  // tokens of a half tile
+    const paged::Tiling tl{2 * HT, HT, kPairCost, kSingleCost, kSmallCost, kTileCost, kWhole};
+    const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, tl, kMinUnits, sm.plan, sm.scratch, a.err);
     if (threadIdx.x == 0) sm.pl = pl;
     ptx::tc_fence_before();
     __syncthreads();
@@ -234,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) ptx::setmaxnreg_dec<kRegsLow>();
     if (warp == 0) {
         // ------------------------------------------------------ loader --
-        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, TQ, HT, wwait)) fail();
+        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, tl, wwait)) fail();
     } else if (warp == 1) {
         // ------------------------------------------------------ issuer --
         const uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(kRows, kKB) : ptx::idesc_bf16_f32(kRows, kKB, false, false);
@@ -300,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // O_w += P V in two halves of 64 keys, the last 64 first: they
                 // run while the softmax warps work on the other half's P
                 ptx::umma_ts4_mn(o_t, p_t + 32u, ptx::mnmajor_desc(v_s, 4), idesc_pv, i >= 2 ? 1u : 0u);
+                if (!kCodes) ptx::umma_commit_w(ptx::smem_u32(&sm.pv_half[w]));
                 const bool next = i + 2 < N;
                 ok = (!next || s_ready(i + 2)) && wwait(&sm.p_full[w], par);
                 if (!ok) break;
@@ -348,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ----------------- Q in two terms, V's codes -> bf16 tiles --
         if constexpr (kCodes) {
             const int cw = warp - 2;
-            int vn = 0, qn = 0;
+            int vn = 0;
+            int qn = 0;
             bool ok = true;
             for (int si = 0; ok; ++si) {
                 Desc d;
@@ -357,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 if (d.done) break;
-                const int n = d.b1 - d.b0;
-                if (n <= 0) continue;
+                if (d.b1 <= d.b0) continue;
                 for (int t = 0; ok && t < (d.pair ? 2 : 1); ++t, ++qn) {
                     const int qs = qn & 1;
                     ok = wwait(&sm.q_raw[qs], (qn >> 1) & 1);
@@ -368,36 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::fence_proxy_async_smem();
                     arrive1(&sm.q_full[qs]);
                 }
-                for (int j = 0; ok && j < n; ++j, ++vn) {
+                for (int j = d.b0; ok && j < d.b1; ++j, ++vn) {
                     const int s = vn & 1;
                     ok = wwait(&sm.st_full[s], (vn >> 1) & 1) && (vn < 2 || wwait(&sm.v_empty[s], ((vn >> 1) - 1) & 1));
                     if (!ok) break;
-                    // lanes of a quarter warp take eight rows: loads and stores
-                    // of the swizzled tiles then touch every bank once
-                    const int r7 = lane & 7, c = lane >> 3;
-                    const uint8_t* from = sm.st[s] + (cw * 64 + r7) * 128 + ((c ^ r7) << 4);
-                    const uint32_t to = ptx::smem_u32(sm.v[s]) + (uint32_t)((cw * 64 + r7) * 128 + (((2 * c) ^ r7) << 4));
-                    const uint32_t to2 = to ^ 16u;
-                    const uint8_t* from2 = sm.st[s] + (cw * 64 + r7) * 128 + (((c + 4) ^ r7) << 4);
-#pragma unroll 1
-                    for (int i0 = 0; i0 < 16; i0 += 4) {
-                        uint4 u[4];  // 16 codes each: features 64 half + 16 c ..., of rows 8 apart
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            u[i] = *reinterpret_cast<const uint4*>((i & 1 ? from2 : from) + ((i0 + i) >> 1) * 1024);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t y[8];
-                            codes_to_bf16(u[i].x, y[0], y[1]);
-                            codes_to_bf16(u[i].y, y[2], y[3]);
-                            codes_to_bf16(u[i].z, y[4], y[5]);
-                            codes_to_bf16(u[i].w, y[6], y[7]);
-                            const uint32_t at = (i & 1) * kHalfBytes + ((i0 + i) >> 1) * 1024;
-                            ptx::st_shared_v4(to + at, y[0], y[1], y[2], y[3]);
-                            ptx::st_shared_v4(to2 + at, y[4], y[5], y[6], y[7]);
-                        }
-                    }
-                    ptx::fence_proxy_async_smem();
+                    convert_v(sm.st[s], ptx::smem_u32(sm.v[s]), cw);
                     arrive1(&sm.v_full[s]);
                     if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.st_empty[s]));
                 }
@@ -413,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sbuf = tmem + lane_base + kColS + (uint32_t)wg * kKB;
         const uint32_t obuf = tmem + lane_base + kColO + (uint32_t)wg * kD;
         uint32_t s_par = 0, e_uses = 0, pv_par = 0;
-        int blk = 0;
+        int blk = 0, it = 0;  // blocks, items of this warpgroup so far
         bool ok = true;
         // all 8 softmax warps meet (arrive, then a bounded wait)
         auto meet = [&]() -> bool {
@@ -447,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!busy) {
                     arrive1(&sm.p_half[wg]);
                     arrive1(&sm.p_full[wg]);
+                    ++it;
                     continue;
                 }
                 ptx::tc_fence_after();
@@ -506,34 +521,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return ptx::max3(m8[0], m8[1], fmaxf(m8[2], m8[3]));
                 };
-                // The row's maximum, of all 128 scores; the last 64 stay in
-                // registers, the first 64 are loaded again: all of them would
-                // not fit beside the rest.
-                uint32_t ya[32], yb[32], yc[32], yd[32];
-                ptx::tmem_ld32(sbuf, ya);
-                ptx::tmem_ld32(sbuf + 32, yb);
-                ptx::tmem_wait_ld();
-                ptx::tmem_ld32(sbuf + 64, yc);
-                ptx::tmem_ld32(sbuf + 96, yd);
-                scaled(ya, 0);
-                scaled(yb, 1);
-                float mx = fmaxf(top(ya), top(yb));
-                ptx::tmem_wait_ld();
-                ptx::tmem_ld32(sbuf, ya);
-                scaled(yc, 2);
-                scaled(yd, 3);
-                mx = ptx::max3(mx, top(yc), top(yd)) * row_mul;
-                const float m_new = fmaxf(m_run, mx);
-                const bool need = m_new > m_run + kRescaleLog2;
-                const float m_use = need ? m_new : m_run;
-                const float corr = need ? ptx::ex2(m_run - m_new) : 1.f;
-                const float base = m_use == -INFINITY ? 0.f : m_use;  // nothing seen yet: weights 2^-inf
-                const float2 nm = make_float2(-base, -base);
-                float2 sum4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+                // The weights' base: the running maximum, which moves only when
+                // a half block's scores pass it by more than 2^8.  A warp that
+                // has such a row rescales O_w and the sums.
+                float2 nm;
+                auto set_base = [&]() {
+                    const float base = m_run == -INFINITY ? 0.f : m_run;  // nothing seen yet: weights 2^-inf
+                    nm = make_float2(-base, -base);
+                };
+                auto move_base = [&](float mx, bool has_o) {
+                    const bool need = mx > m_run + kRescaleLog2;
+                    const float corr = need ? ptx::ex2(m_run - mx) : 1.f;
+                    l_run *= corr;
+                    m_run = need ? mx : m_run;
+                    if (has_o) {
+#pragma unroll 1
+                        for (int b = 0; b < 8; ++b) {
+                            uint32_t o[16];
+                            ptx::tmem_ld16(obuf + (uint32_t)b * 16, o);
+                            ptx::tmem_wait_ld();
+                            ptx::reg_fence16(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                            ptx::tmem_st16(obuf + (uint32_t)b * 16, o);
+                        }
+                    }
+                };
                 // columns 32 c ... -> P, bf16 pairs in columns 64 + 16 c ... of the
                 // buffer (behind the scores that are still to be loaded again)
                 auto weigh = [&](const uint32_t(&y)[32], int c) {
                     uint32_t pk[16];
+                    float2 sum4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
                     float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -557,40 +575,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     ptx::tmem_st16(sbuf + 64u + 16u * c, pk);
+                    const float2 s2 = ptx::add2(ptx::add2(sum4[0], sum4[1]), ptx::add2(sum4[2], sum4[3]));
+                    l_run += s2.x + s2.y;
                 };
-                weigh(yc, 2);
-                weigh(yd, 3);
-                if (j > j0 && __any_sync(0xffffffffu, need)) {
-                    // rescale O_w before this item's P V adds to it: S of this
-                    // item was committed after the P V of the previous one, so
-                    // that is done
-#pragma unroll 1
-                    for (int b = 0; b < 8; ++b) {
-                        uint32_t o[16];
-                        ptx::tmem_ld16(obuf + (uint32_t)b * 16, o);
-                        ptx::tmem_wait_ld();
-                        ptx::reg_fence16(o);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-                        ptx::tmem_st16(obuf + (uint32_t)b * 16, o);
+                // P is handed to the issuer in two halves of 64 keys, the last
+                // 64 first.  bf16: each half's maximum just before its weights,
+                // so that the first products start early (a frame over 24
+                // frames: 422 us, against 437 with the maximum of all first).
+                // Codes: the maximum of all first, the first 64 scores loaded
+                // again (two streams' frames: 371 us, against 440 the other
+                // way: the scales' loads then compete with the products'
+                // operands for shared memory).
+                auto over = [&](float mx) { return __any_sync(0xffffffffu, mx > m_run + kRescaleLog2); };
+                if constexpr (kCodes) {
+                    uint32_t ya[32], yb[32], yc[32], yd[32];
+                    ptx::tmem_ld32(sbuf, ya);
+                    ptx::tmem_ld32(sbuf + 32, yb);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(sbuf + 64, yc);
+                    ptx::tmem_ld32(sbuf + 96, yd);
+                    scaled(ya, 0);
+                    scaled(yb, 1);
+                    float mx = fmaxf(top(ya), top(yb));
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(sbuf, ya);
+                    scaled(yc, 2);
+                    scaled(yd, 3);
+                    mx = ptx::max3(mx, top(yc), top(yd)) * row_mul;
+                    if (over(mx)) move_base(mx, j > j0);
+                    set_base();
+                    weigh(yc, 2);
+                    weigh(yd, 3);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(sbuf + 32, yb);
+                    scaled(ya, 0);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    arrive1(&sm.p_half[wg]);
+                    weigh(ya, 0);
+                    ptx::tmem_wait_ld();
+                    scaled(yb, 1);
+                    weigh(yb, 1);
+                } else {
+                    uint32_t ya[32], yb[32];
+                    ptx::tmem_ld32(sbuf + 64, ya);
+                    ptx::tmem_ld32(sbuf + 96, yb);
+                    ptx::tmem_wait_ld();
+                    scaled(ya, 2);
+                    scaled(yb, 3);
+                    float mx = fmaxf(top(ya), top(yb)) * row_mul;
+                    // (S of this item was committed after the P V of the previous one: O_w is still)
+                    if (over(mx)) move_base(mx, j > j0);
+                    set_base();
+                    weigh(ya, 2);
+                    ptx::tmem_ld32(sbuf, ya);
+                    weigh(yb, 3);
+                    ptx::tmem_ld32(sbuf + 32, yb);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    arrive1(&sm.p_half[wg]);
+                    ptx::tmem_wait_ld();
+                    scaled(ya, 0);
+                    scaled(yb, 1);
+                    mx = fmaxf(top(ya), top(yb)) * row_mul;
+                    if (over(mx)) {
+                        ok = wwait(&sm.pv_half[wg], it & 1);  // the first half's P V is in O_w
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        move_base(mx, true);
+                        set_base();
                     }
+                    weigh(ya, 0);
+                    weigh(yb, 1);
                 }
-                ptx::tmem_wait_ld();
-                ptx::tmem_ld32(sbuf + 32, yb);
-                scaled(ya, 0);
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before();
-                arrive1(&sm.p_half[wg]);
-                weigh(ya, 0);
-                ptx::tmem_wait_ld();
-                scaled(yb, 1);
-                weigh(yb, 1);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 arrive1(&sm.p_full[wg]);
-                const float2 s2 = ptx::add2(ptx::add2(sum4[0], sum4[1]), ptx::add2(sum4[2], sum4[3]));
-                l_run = l_run * corr + (s2.x + s2.y);
-                m_run = m_use;
+                ++it;
             }
             if (!ok) break;
             blk += n;

@@ -158,8 +158,8 @@ __device__ __forceinline__ void split_q(uint8_t* tile, float* row_scale, int row
 // either way.
 template <bool kCodes, class S, class Wait>
 __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                                            const CUtensorMap& tm_v, const PagedAttend& a, const Plan& pl, int TQ,
-                                            int HT, Wait wwait) {
+                                            const CUtensorMap& tm_v, const PagedAttend& a, const Plan& pl,
+                                            const Tiling& tl, Wait wwait) {
     const PagedGeom& g = a.g;
     const int lane = threadIdx.x & 31;
     const int no_abort = 0;
@@ -189,8 +189,8 @@ __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, cons
             arrive1(&sm.d_full[slot]);
             break;
         }
-        const Piece pc = piece_at<kKB>(a.mask, sm.plan, pl, cur, TQ, HT);
-        const bool pair = pc.n > HT;
+        const Piece pc = piece_at<kKB>(a.mask, sm.plan, pl, cur, tl);
+        const bool pair = pc.n > tl.half;
         const int at0 = pc.q.total - pc.q.n + pc.i0;
         if (lane == 0)
             sm.desc[slot] = Desc{0,          cur.s,        cur.h,        pc.q.q0 + pc.i0, pc.n, at0,
@@ -207,8 +207,8 @@ __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, cons
                 }
                 const uint32_t bar = ptx::smem_u32(sm.q_landed(qs));
                 const uint32_t dst = ptx::smem_u32(sm.q[qs]);
-                ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(HT * g.G) * 256u);
-                const int row = pc.q.q0 + pc.i0 + t * HT;
+                ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(tl.half * g.G) * 256u);
+                const int row = pc.q.q0 + pc.i0 + t * tl.half;
                 ptx::tma_load_4d_w(dst, &tm_q, 0, cur.h * g.G, row, 0, bar);
                 ptx::tma_load_4d_w(dst + S::kQHalf, &tm_q, 64, cur.h * g.G, row, 0, bar);
             }
@@ -304,7 +304,7 @@ __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, cons
                 }
             }
         }
-        more = advance(sm.plan, pl, a.seqs, TQ, pc.units, cur);
+        more = advance(sm.plan, pl, a.seqs, tl, pc.units, cur);
     }
             // the last loads of each ring have landed before exit
     auto landed = [&](uint64_t* bar, int use) {
