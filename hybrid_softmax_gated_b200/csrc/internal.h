@@ -22,6 +22,25 @@ enum : int {
     kErrTimeoutTokenLevel = 1 << 2,
 };
 
+// Launch with programmatic stream serialization: the kernel may start while
+// the one before it in the stream drains, so it waits for that one
+// (griddepcontrol.wait, ptx::pdl_wait_then_trigger) before it touches global
+// memory.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---- failure path self-test (simt.cu) -------------------------------------
 // One thread waits for *flag to become nonzero with the same bounded spin
 // the kernels' inter-CTA waits use; after limit_ns it sets kErrTimeoutAttn

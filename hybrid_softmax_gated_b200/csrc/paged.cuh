@@ -46,13 +46,14 @@ struct Sight {
 };
 __device__ __forceinline__ Sight sight(const PagedMask& m, int at, int total) {
     if (at < 0) return Sight{0, 0, 0};
-    const long long e = ((long long)(at / m.block) + 1) * m.block;
+    // (positions and blocks stay below 2^30 + 1: e below 2^31 + 1)
+    const uint32_t e = m.block == 1 ? (uint32_t)at + 1u : ((uint32_t)at / (uint32_t)m.block + 1u) * (uint32_t)m.block;
     Sight s;
-    s.end = (int)(e < total ? e : total);
+    s.end = (int)min(e, (uint32_t)total);
     s.lo = 0;
     s.sink = 0;
     if (m.window) {
-        s.lo = (int)(e - m.window < 0 ? 0 : e - m.window);
+        s.lo = e < (uint32_t)m.window ? 0 : (int)(e - (uint32_t)m.window);
         s.sink = m.sinks < s.end ? m.sinks : s.end;
     }
     return s;
@@ -98,6 +99,7 @@ struct PlanSmem {
     int q_off[kPagedMaxSeqs + 1];
     int total[kPagedMaxSeqs];
     long long warp_sum[32];
+    int warp_tiles[32];
     long long start_base;          // units of the head before the first tile
     int start_seq, start_tile;
     long long start, end;          // the CTA's first unit and its last + 1, of their heads
@@ -114,26 +116,32 @@ struct Plan {
     Cursor first;
 };
 
-// Exclusive prefix over the block's threads; *all gets the sum.
-__device__ __forceinline__ long long block_prefix(long long v, PlanSmem& ps, long long* all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    long long x = v;
+// Exclusive prefix over the block's threads (32 warps at most); *all gets the sum.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) ps.warp_sum[warp] = x;
+    return x;
+}
+template <typename T>
+__device__ __forceinline__ T block_prefix(T v, T* warp_sum, T* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const T x = warp_scan(v);
+    if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    long long before = 0, sum = 0;
-    for (int w = 0; w < warps; ++w) {
-        const long long y = ps.warp_sum[w];
-        if (w < warp) before += y;
-        sum += y;
-    }
-    __syncthreads();
-    *all = sum;
-    return before + x - v;
+    const T sums = warp_scan(lane < warps ? warp_sum[lane] : (T)0);
+    *all = __shfl_sync(0xffffffffu, sums, 31);
+    const T before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : (T)0) + x - v;
+}
+// a b / c and a / c, in 32 bits where they fit (64-bit divisions cost hundreds of cycles)
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+    const unsigned long long p = (unsigned long long)a * (unsigned)b;
+    return p >> 32 || c >> 32 ? (long long)(p / (unsigned long long)c) : (long long)((uint32_t)p / (uint32_t)c);
 }
 
 __device__ __forceinline__ Seq seq_of(const PlanSmem& ps, int s) {
@@ -183,9 +191,8 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
         mine += (q.n + tl.tokens - 1) / tl.tokens;
     }
     if (tid == 0) ps.q_off[b.S] = b.q_off[b.S];
-    long long all;
-    const int before = (int)block_prefix(mine, ps, &all);
-    const int n_tiles = (int)all;
+    int n_tiles;
+    const int before = block_prefix(mine, ps.warp_tiles, &n_tiles);
     for (int s = s0; s < s1; ++s) tiles[s] += before;
     if (tid == 0) tiles[b.S] = n_tiles;
     __syncthreads();
@@ -211,22 +218,23 @@ __device__ Plan make_plan(const PagedGeom& g, const PagedSeqs& b, const PagedMas
         while (f >= tiles[s + 1]) ++s;
         sum += units_of<KB>(m, seq_of(ps, s), f - tiles[s], tl);
     }
-    const long long pre = block_prefix(sum, ps, &all);
+    long long all;
+    const long long pre = block_prefix(sum, ps.warp_sum, &all);
     pl.U = all * g.Hk;
     pl.P = gridDim.x;
     if (pl.U < (long long)pl.P * min_units) pl.P = pl.U < min_units ? 1 : (int)(pl.U / min_units);
     if ((int)blockIdx.x >= pl.P) return pl;
-    pl.u0 = pl.U * blockIdx.x / pl.P;
-    pl.u1 = pl.U * (blockIdx.x + 1) / pl.P;
+    pl.u0 = mul_div(pl.U, blockIdx.x, pl.P);
+    pl.u1 = mul_div(pl.U, blockIdx.x + 1, pl.P);
     // the tiles under both borders
-    const int h0 = (int)(pl.u0 / all), h1 = (int)(pl.u1 / all);
+    const int h0 = (int)mul_div(pl.u0, 1, all), h1 = (int)mul_div(pl.u1, 1, all);
     const long long rem0 = pl.u0 - h0 * all, rem1 = pl.u1 - h1 * all;
     const bool has0 = rem0 >= pre && rem0 < pre + sum, has1 = rem1 >= pre && rem1 < pre + sum && rem1 > 0;
     if (has0 || has1) {
         long long at = pre;
         for (int f = f0, s = s_first; f < f1; ++f) {
             while (f >= tiles[s + 1]) ++s;
-            const int u = units_of<KB>(m, seq_of(ps, s), f - tiles[s], tl);
+            const int u = f1 - f0 == 1 ? (int)sum : units_of<KB>(m, seq_of(ps, s), f - tiles[s], tl);
             if (has0 && rem0 >= at && rem0 < at + u) {
                 ps.start_base = at;
                 ps.start_seq = s;
@@ -273,7 +281,7 @@ __device__ __forceinline__ Piece piece_at(const PagedMask& m, const PlanSmem& ps
         p.c0 = p.c1 = blockIdx.x;
     } else {
         p.c0 = (int)(((c.base + 1) * pl.P - 1) / pl.U);
-        if (pl.U * (p.c0 + 1) / pl.P - c.base <= tl.tile_cost) ++p.c0;  // (that border moved to the tile's start)
+        if (mul_div(pl.U, p.c0 + 1, pl.P) - c.base <= tl.tile_cost) ++p.c0;  // (that border moved to the tile's start)
         p.c1 = (int)(((c.base + p.units) * pl.P - 1) / pl.U);
     }
     return p;
@@ -299,7 +307,7 @@ __device__ __forceinline__ bool advance(const PlanSmem& ps, const Plan& pl, cons
 // 0 if the tile reaches back to or before the CTA's first unit, else 1 (a CTA
 // has at most one cut tile at each end).
 __device__ __forceinline__ int partial_slot(const Plan& pl, int c, long long base) {
-    return 2 * c + (pl.U * c / pl.P >= base ? 0 : 1);
+    return 2 * c + (mul_div(pl.U, c, pl.P) >= base ? 0 : 1);
 }
 
 template <typename T>

@@ -49,7 +49,7 @@ constexpr int kThreads = 384;
 constexpr int kN = 16;                    // columns of a term (query rows)
 // For the schedule, in blocks: what a tile costs on top of its blocks, up to
 // what it is not cut, and how much a CTA has at least.
-constexpr int kTileCost = 4, kWhole = 8, kMinUnits = 6;
+constexpr int kTileCost = 4, kWhole = 16, kMinUnits = 8;
 static_assert(kMinUnits > kTileCost, "one border at most in what a tile costs for itself");
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColS = 0, kColO = 128;  // four S buffers of 32 columns; O_0, O_1 of 64
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
+    ptx::pdl_wait_then_trigger();  // (nothing before this touches global memory)
     const paged::Tiling tl{NR / g.G, NR / g.G, 1, 1, 1, kTileCost, kWhole};
     const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, tl, kMinUnits, sm.plan, sm.scratch, a.err);
     if (threadIdx.x == 0) sm.pl = pl;
@@ -597,21 +598,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (sm.last) {
                     __threadfence();
-                    for (int row = r0; row < r0 + NR / 2 && row < rows; ++row) {
-                        auto ml_at = [&](int cta) {
-                            return __ldcg(a.work.ml + (size_t)paged::partial_slot(sm.pl, cta, d.base) * kN + row);
-                        };
-                        float m = -INFINITY;
-                        for (int i = d.c0; i <= d.c1; ++i) m = fmaxf(m, ml_at(i).x);
-                        float lsum = 0.f, o = 0.f;
-                        for (int i = d.c0; i <= d.c1; ++i) {
-                            const float2 ml = ml_at(i);
-                            const float w = ml.x == -INFINITY ? 1.f : ptx::ex2(ml.x - m);
-                            lsum = fmaf(w, ml.y, lsum);
-                            o = fmaf(w, __ldcg(a.work.o + ((size_t)paged::partial_slot(sm.pl, i, d.base) * kN + row) * kD + at), o);
-                        }
-                        out[out_at(row) + at] = __float2bfloat16_rn(lsum == 0.f ? 0.f : o / lsum);
+                    // one pass over the pieces, all rows' loads in flight together
+                    constexpr int R = NR / 2;
+                    float mm[R], ll[R], oo[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        mm[r] = -INFINITY;
+                        ll[r] = oo[r] = 0.f;
                     }
+#pragma unroll 2
+                    for (int i = d.c0; i <= d.c1; ++i) {
+                        const size_t at_row = (size_t)paged::partial_slot(sm.pl, i, d.base) * kN + r0;
+                        float2 ml[R];
+                        float o[R];
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {  // (rows past the tile's: of earlier use, not written out)
+                            ml[r] = __ldcg(a.work.ml + at_row + r);
+                            o[r] = __ldcg(a.work.o + (at_row + r) * kD + at);
+                        }
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const float m = fmaxf(mm[r], ml[r].x);
+                            // (weights without a maximum are NaN or none)
+                            const float w0 = mm[r] == -INFINITY ? 1.f : ptx::ex2(mm[r] - m);
+                            const float w1 = ml[r].x == -INFINITY ? 1.f : ptx::ex2(ml[r].x - m);
+                            ll[r] = ll[r] * w0 + ml[r].y * w1;
+                            oo[r] = oo[r] * w0 + o[r] * w1;
+                            mm[r] = m;
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (r0 + r < rows)
+                            out[out_at(r0 + r) + at] = __float2bfloat16_rn(ll[r] == 0.f ? 0.f : oo[r] / ll[r]);
                 }
             } else {
                 // (red_l and red_c have been read: the next piece may write them)
@@ -656,8 +675,8 @@ cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int grid = max_ctas > 0 && max_ctas < sms ? max_ctas : sms;
     static_assert(2 * kN <= kPagedRowsPerSm, "workspace rows");
-    paged_few_kernel<kCodes, NR><<<grid, kThreads, sizeof(Smem<kCodes>), st>>>(q, k, v, a, a.scale * 1.4426950408889634f);
-    return cudaGetLastError();
+    return launch_pdl(paged_few_kernel<kCodes, NR>, grid, kThreads, sizeof(Smem<kCodes>), st, q, k, v, a,
+                      a.scale * 1.4426950408889634f);
 }
 
 template <bool kCodes>

@@ -10,6 +10,7 @@
 // their loads in flight together; it finds the token's sequence by a 32-way
 // search of the offsets (one load for up to 32 sequences, two for 1024).
 #include "paged.cuh"
+#include "ptx.cuh"
 
 #include <type_traits>
 
@@ -150,6 +151,7 @@ __device__ __forceinline__ float scale_of(float amax, bool finite) {
 template <typename T, bool kCodes, int kLanes>
 __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool pool, PagedSeqs b, const T* k,
                                                          long long k_stride, const T* v, long long v_stride, int* err) {
+    ptx::pdl_wait_then_trigger();
     constexpr int kRow = kLanes ? kLanes : 32, kPer = 32 / kRow;
     const int rows = 2 * g.Hk;
     const Share sh = share_of(rows, kSteps * kPer);
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool 
 template <typename T, bool kCodes, int kLanes>
 __global__ void __launch_bounds__(kThreads) read_kernel(PagedGeom g, PagedPool pool, PagedSeqs b, const int* starts,
                                                         T* k, T* v, int* err) {
+    ptx::pdl_wait_then_trigger();
     constexpr int kRow = kLanes ? kLanes : 32, kPer = 32 / kRow;
     const int rows = 2 * g.Hk;
     const Share sh = share_of(rows, kSteps * kPer);
@@ -331,9 +334,8 @@ cudaError_t write_as(const PagedGeom& g, const PagedPool& pool, const PagedSeqs&
     constexpr int n = Lane16<T>::n;
     const bool fits = aligned16(k) && aligned16(v) && ks % n == 0 && vs % n == 0;
     auto go = [&](auto kernel, int lanes) {
-        kernel<<<blocks_for(b.tokens, g.Hk, 32 / lanes), kThreads, 0, st>>>(g, pool, b, static_cast<const T*>(k), ks,
-                                                                          static_cast<const T*>(v), vs, err);
-        return cudaGetLastError();
+        return launch_pdl(kernel, blocks_for(b.tokens, g.Hk, 32 / lanes), kThreads, 0, st, g, pool, b,
+                          static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, err);
     };
     if (fits && g.d == 128) return go(write_kernel<T, kCodes, 128 / n>, 128 / n);
     if (fits && g.d == 64) return go(write_kernel<T, kCodes, 64 / n>, 64 / n);
@@ -346,9 +348,8 @@ cudaError_t read_as(const PagedGeom& g, const PagedPool& pool, const PagedSeqs& 
     constexpr int n = Lane16<T>::n;
     const bool fits = aligned16(k) && aligned16(v);
     auto go = [&](auto kernel, int lanes) {
-        kernel<<<blocks_for(b.tokens, g.Hk, 32 / lanes), kThreads, 0, st>>>(g, pool, b, starts, static_cast<T*>(k),
-                                                                          static_cast<T*>(v), err);
-        return cudaGetLastError();
+        return launch_pdl(kernel, blocks_for(b.tokens, g.Hk, 32 / lanes), kThreads, 0, st, g, pool, b, starts,
+                          static_cast<T*>(k), static_cast<T*>(v), err);
     };
     if (fits && g.d == 128) return go(read_kernel<T, kCodes, 128 / n>, 128 / n);
     if (fits && g.d == 64) return go(read_kernel<T, kCodes, 64 / n>, 64 / n);

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
+    ptx::pdl_wait_then_trigger();  // (nothing before this touches global memory)
     const int HT = kRows / g.G;  // tokens of a half tile
     const paged::Tiling tl{2 * HT, HT, kPairCost, kSingleCost, kSmallCost, kTileCost, kWhole};
     const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, tl, kMinUnits, sm.plan, sm.scratch, a.err);
@@ -866,9 +867,8 @@ cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int grid = max_ctas > 0 && max_ctas < sms ? max_ctas : sms;
     static_assert(2 * 2 * kRows <= kPagedRowsPerSm, "workspace rows");
-    paged_tc_kernel<kCodes><<<grid, kThreads, sizeof(Smem<kCodes>), st>>>(
-        q, k, v, a, a.scale * 1.4426950408889634f);
-    return cudaGetLastError();
+    return launch_pdl(paged_tc_kernel<kCodes>, grid, kThreads, sizeof(Smem<kCodes>), st, q, k, v, a,
+                      a.scale * 1.4426950408889634f);
 }
 
 }  // namespace

@@ -13,6 +13,7 @@
 // sines, once each, into shared memory.
 #include "arl2.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 #include <cmath>
 #include <cstdint>
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     using F = Form<T, kHalves, kWide>;
     using R = typename RawOf<F::kBytes>::type;
     extern __shared__ float2 cs[];  // [token][pair]
+    ptx::pdl_wait_then_trigger();
     const int half = plan.rot >> 1, d = plan.d;
     const int tok0 = blockIdx.x * per_block;
     const int n_tok = min(per_block, tokens - tok0);
@@ -212,9 +214,8 @@ cudaError_t launch_as(const Plan& p, const Side& q, const Side& k, const int* po
     int per_block = kThreads / (per_head * groups);
     per_block = per_block < 1 ? 1 : per_block > kMaxTokensPerBlock ? kMaxTokensPerBlock : per_block;
     const int grid = (tokens + per_block - 1) / per_block;
-    rotary_kernel<T, kHalves, kWide>
-        <<<grid, kThreads, (size_t)per_block * (p.rot / 2) * sizeof(float2), st>>>(p, q, k, pos, tokens, per_block, group, sign);
-    return cudaGetLastError();
+    return launch_pdl(rotary_kernel<T, kHalves, kWide>, grid, kThreads, (size_t)per_block * (p.rot / 2) * sizeof(float2),
+                      st, p, q, k, pos, tokens, per_block, group, sign);
 }
 
 template <typename T, bool kHalves>
