@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto init = [](uint64_t* b, int n) { ptx::mbar_init(ptx::smem_u32(b), n); };
         for (int i = 0; i < kDescs; ++i) {
             init(&sm.d_full[i], 1);
-            init(&sm.d_empty[i], 1 + kSoftmaxWarps + 1 + (kCodes ? 1 : 0));
+            init(&sm.d_empty[i], 1 + kSoftmaxWarps + 2);
             init(&sm.s_full[i], 1);
             init(&sm.s_taken[i], kWgWarps);
         }
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ loader --
-        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, tl, wwait)) fail();
+        if (!paged::load_pieces<kCodes, false>(sm, tm_q, tm_k, tm_v, a, pl, tl, wwait)) fail();
     } else if (warp == 1) {
         // ------------------------------------------------------ issuer --
         // A: K (K-major) or V (MN-major), 128 rows; B: Q or P (K-major), 16 rows a term
@@ -309,28 +309,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) fail();
     } else if (warp == 3) {
-        // ---------------------------------------------- Q in two terms --
-        if constexpr (kCodes) {
-            int qn = 0;
-            bool ok = true;
-            for (int si = 0; ok; ++si) {
-                Desc d;
-                if (!get_desc(si, d)) {
-                    ok = false;
-                    break;
-                }
-                if (d.done) break;
-                if (d.b1 <= d.b0) continue;
+        // ------------------------- V's loader; codes: Q in two terms --
+        // (one warp for all loads would take 1560 cycles a block of codes: more
+        // than the block's way from memory)
+        ptx::tma_prefetch_desc(&tm_v);
+        paged::Loader<kCodes, S> ld{sm, a, tm_q, tm_k, tm_v};
+        int qn = 0;
+        bool ok = true;
+        for (int si = 0; ok; ++si) {
+            Desc d;
+            if (!get_desc(si, d)) {
+                ok = false;
+                break;
+            }
+            if (d.done) break;
+            const int n = d.b1 - d.b0;
+            if (n <= 0) continue;
+            paged::Places at(a, d);
+            auto split = [&]() -> bool {
                 const int qs = qn & 1;
-                ok = wwait(&sm.q_raw[qs], (qn >> 1) & 1);
-                if (!ok) break;
+                if (!wwait(&sm.q_raw[qs], (qn >> 1) & 1)) return false;
                 paged::split_q<S::kQHalf>(sm.q[qs], sm.row_scale[qn & 3], d.n * g.G, 0, 1, scale_log2);
                 ptx::fence_proxy_async_smem();
                 arrive1(&sm.q_full[qs]);
                 ++qn;
+                return true;
+            };
+            for (int j = 0; ok && j < n; ++j) {
+                ok = ld.load_v(at, j, wwait);
+                at.done(j);
+                // (Q has landed by the time the first blocks are on their way)
+                if (kCodes && ok && (j == 1 || j == n - 1 && j < 1)) ok = split();
             }
-            if (!ok) fail();
         }
+        ld.drain();
+        if (!ok) fail();
     } else if (warp >= 4) {
         // ------------------------------------------ softmax, epilogue --
         const int wg = (warp - 4) >> 2, ww = warp & 3;  // ww: TMEM lanes 32 ww ..

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) ptx::setmaxnreg_dec<kRegsLow>();
     if (warp == 0) {
         // ------------------------------------------------------ loader --
-        if (!paged::load_pieces<kCodes>(sm, tm_q, tm_k, tm_v, a, pl, tl, wwait)) fail();
+        if (!paged::load_pieces<kCodes, true>(sm, tm_q, tm_k, tm_v, a, pl, tl, wwait)) fail();
     } else if (warp == 1) {
         // ------------------------------------------------------ issuer --
         const uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(kRows, kKB) : ptx::idesc_bf16_f32(kRows, kKB, false, false);

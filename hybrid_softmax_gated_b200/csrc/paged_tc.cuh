@@ -151,32 +151,203 @@ __device__ __forceinline__ void split_q(uint8_t* tile, float* row_scale, int row
     }
 }
 
+// Where a piece's blocks lie: their pages' places in the pool (page x heads +
+// head, or `absent`, which reads as zeros), one page per lane for a batch of
+// blocks at a time; a batch is looked up two batches before it is needed, so
+// nobody waits for the page table.  The whole warp.
+struct Places {
+    const PagedAttend* a;
+    const Desc* d;
+    int n, pb_log2, batch_log2, span, absent;  // blocks; pages of a block, blocks of a batch, keys of a page's share
+    int see_lo;
+    Sight last;      // keys that some query sees: [0, last.sink) and [see_lo, last.end)
+    int at;          // batch of p0
+    int p0, p1, raw; // places of batches at and at + 1; what the table says of at + 2
+    bool need;
+
+    __device__ __forceinline__ int per_block() const { return 1 << pb_log2; }
+    __device__ __forceinline__ int slot0(int j) const { return d->key0(j) & ((1 << a->g.page_log2) - 1); }
+    __device__ __forceinline__ void look_up(int batch) {
+        const int lane = threadIdx.x & 31, j = (batch << batch_log2) + (lane >> pb_log2);
+        const int k0 = d->key0(j) + ((lane & (per_block() - 1)) << a->g.page_log2);
+        need = j < n && k0 < last.end && (k0 + span > see_lo || k0 < last.sink);
+        raw = need ? a->seqs.table[(size_t)d->s * a->seqs.max_pages + (k0 >> a->g.page_log2)] : 0;
+    }
+    __device__ __forceinline__ int found() const {
+        if (!need) return absent;
+        if ((unsigned)raw < (unsigned)a->g.pages) return raw * a->g.Hk + d->h;
+        report(a->err, kErrPagedTable);
+        return absent;
+    }
+    __device__ __forceinline__ Places(const PagedAttend& a_, const Desc& d_) : a(&a_), d(&d_) {
+        const int page_tokens = 1 << a->g.page_log2;
+        n = d->b1 - d->b0;
+        pb_log2 = page_tokens < kKB ? 7 - a->g.page_log2 : 0;
+        batch_log2 = 5 - pb_log2;
+        span = page_tokens < kKB ? page_tokens : kKB;
+        absent = a->g.pages * a->g.Hk;
+        last = sight(a->mask, d->at0 + d->n - 1, d->total);
+        see_lo = sight(a->mask, d->at0 < 0 ? 0 : d->at0, d->total).lo;
+        at = 0;
+        look_up(0);
+        const bool n0 = need;
+        const int r0 = raw;
+        look_up(1);
+        const bool n1 = need;
+        const int r1 = raw;
+        look_up(2);
+        const bool n2 = need;
+        const int r2 = raw;
+        need = n0, raw = r0;
+        p0 = found();
+        need = n1, raw = r1;
+        p1 = found();
+        need = n2, raw = r2;
+    }
+    // place of this lane's page of block j, in batch `at` or the next one (lanes
+    // past the block's pages: any)
+    __device__ __forceinline__ int of(int j) const {
+        const int src = ((j << pb_log2) & 31) + ((threadIdx.x & 31) & (per_block() - 1));
+        return __shfl_sync(0xffffffffu, (j >> batch_log2) > at ? p1 : p0, src);
+    }
+    // block j (and all before it) is done with
+    __device__ __forceinline__ void done(int j) {
+        if (((j + 1) & ((1 << batch_log2) - 1)) == 0) {
+            p0 = p1;
+            p1 = found();
+            ++at;
+            look_up(at + 2);
+        }
+    }
+};
+
+// A ring's slot and the parity of its barriers' phase, without divisions.
+template <int kSlots>
+struct Ring {
+    int slot = 0, uses = 0;
+    uint32_t lap = 0;
+    __device__ __forceinline__ bool waits() const { return uses >= kSlots; }
+    __device__ __forceinline__ uint32_t parity() const { return (lap & 1) ^ 1; }  // of the slot's previous lap
+    __device__ __forceinline__ void next() {
+        ++uses;
+        if (++slot == kSlots) {
+            slot = 0;
+            ++lap;
+        }
+    }
+};
+
+template <bool kCodes, class S>
+struct Loader {
+    S& sm;
+    const PagedAttend& a;
+    const CUtensorMap &tm_q, &tm_k, &tm_v;
+    Ring<S::kK> kr;
+    Ring<S::kVLoads> vr;
+    int qn = 0, tails = 0, tail_use = 0;  // (tail_use: the V ring's use that was the last tail)
+
+    // Q tiles of the piece
+    template <class Wait>
+    __device__ __forceinline__ bool load_q(const Desc& d, int half, Wait wwait) {
+        for (int t = 0; t < (d.pair ? 2 : 1); ++t, ++qn) {
+            const int qs = qn & 1;
+            if (qn >= 2 && !wwait(&sm.q_empty[qs], ((qn >> 1) - 1) & 1)) return false;
+            const uint32_t bar = ptx::smem_u32(sm.q_landed(qs)), dst = ptx::smem_u32(sm.q[qs]);
+            ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(half * a.g.G) * 256u);
+            ptx::tma_load_4d_w(dst, &tm_q, 0, d.h * a.g.G, d.row0 + t * half, 0, bar);
+            ptx::tma_load_4d_w(dst + S::kQHalf, &tm_q, 64, d.h * a.g.G, d.row0 + t * half, 0, bar);
+        }
+        return true;
+    }
+    template <class Wait>
+    __device__ __forceinline__ bool load_k(const Places& pl, int j, Wait wwait) {
+        const int lane = threadIdx.x & 31, s = kr.slot, place = pl.of(j), slot0 = pl.slot0(j);
+        if (kr.waits() && !wwait(&sm.k_empty[s], kr.parity())) return false;
+        const uint32_t bar = ptx::smem_u32(&sm.k_full[s]);
+        ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)S::kKBytes);
+        __syncwarp();
+        if (lane < pl.per_block()) {
+            const uint32_t dst = ptx::smem_u32(sm.k[s]) + (uint32_t)(lane << a.g.page_log2) * 128u;
+            ptx::tma_load_4d(dst, &tm_k, 0, slot0, place, 0, bar);
+            if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_k, 64, slot0, place, 0, bar);
+        }
+        __syncwarp();
+        if constexpr (kCodes) {
+            // the scales: 16 bytes per lane and tensor (bulk copies of a page's
+            // scales cost the copy engine as much as its codes: 236 us, against
+            // 201 this way, at 64 streams of 8256 keys)
+            const int of = ((4 * lane) >> a.g.page_log2) & (pl.per_block() - 1);
+            const int there = __shfl_sync(0xffffffffu, place, of);
+            const bool is = there != pl.absent;
+            const size_t row = is ? ((size_t)there << a.g.page_log2) + slot0 + 4 * lane - (of << a.g.page_log2) : 0;
+            const uint32_t to = ptx::smem_u32(sm.ks(kr.uses)) + 16u * lane, bytes = is ? 16u : 0u;  // (absent: zeros, as the codes)
+            ptx::cp_async16(to, a.pool.ks + row, bytes);
+            ptx::cp_async16(to + kKB * 4u, a.pool.vs + row, bytes);
+            ptx::cp_async_arrive(bar);
+        }
+        kr.next();
+        return true;
+    }
+    template <class Wait>
+    __device__ __forceinline__ bool load_v(const Places& pl, int j, Wait wwait) {
+        const int lane = threadIdx.x & 31, s = vr.slot, place = pl.of(j), slot0 = pl.slot0(j);
+        if (vr.waits() && !wwait(sm.v_taken(s), vr.parity())) return false;
+        uint64_t* full = sm.v_landed(s);
+        if (S::kClearTail && j == pl.n - 1 && pl.d->key0(j) + kKB > pl.d->total) {
+            // a warp of its own clears the tail and hands the tile on; one at a
+            // time (the previous one's slot, if not in use again, tells)
+            if (tails && vr.uses - tail_use < S::kVLoads &&
+                !wwait(sm.v_landed(tail_use % S::kVLoads), (tail_use / S::kVLoads) & 1))
+                return false;
+            full = &sm.v_tail;
+            tail_use = vr.uses;
+            ++tails;
+        }
+        const uint32_t bar = ptx::smem_u32(full);
+        ptx::mbar_arrive_expect_tx_w(bar, kCodes ? kCodeTile : kTileBytes);
+        __syncwarp();
+        if (lane < pl.per_block()) {
+            const uint32_t dst = ptx::smem_u32(sm.v_load(s)) + (uint32_t)(lane << a.g.page_log2) * 128u;
+            ptx::tma_load_4d(dst, &tm_v, 0, slot0, place, 0, bar);
+            if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_v, 64, slot0, place, 0, bar);
+        }
+        __syncwarp();
+        vr.next();
+        return true;
+    }
+    // the last loads of each ring have landed (before exit)
+    __device__ __forceinline__ void drain() {
+        const int no_abort = 0;
+        auto landed = [&](uint64_t* bar, int use) {
+            ptx::mbar_wait_bounded(ptx::smem_u32(bar), use & 1, &no_abort, kWaitLimitNs);
+        };
+        for (int i = kr.uses > S::kK ? kr.uses - S::kK : 0; i < kr.uses; ++i) landed(&sm.k_full[i % S::kK], i / S::kK);
+        if (tails) landed(&sm.v_tail, tails - 1);
+        for (int i = vr.uses > S::kVLoads ? vr.uses - S::kVLoads : 0; i < vr.uses; ++i)
+            landed(sm.v_landed(i % S::kVLoads), i / S::kVLoads);
+        for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i) landed(sm.q_landed(i & 1), i >> 1);
+    }
+};
+
 // The loading warp: this CTA's pieces one after the other, their descriptors
-// published to the other roles, their Q tiles and their blocks' pages (found
-// through the page table) loaded by TMA.  S: the kernel's shared memory.  wwait:
-// the bounded wait.  Returns false if one ran out; waits for its own loads
-// either way.
-template <bool kCodes, class S, class Wait>
+// published to the other roles, their Q tiles and their blocks' pages loaded by
+// TMA; with_v: V's too (else a warp of its own loads them, load_values).  S: the
+// kernel's shared memory.  wwait: the bounded wait.  Returns false if one ran
+// out; waits for its own loads either way.
+template <bool kCodes, bool with_v, class S, class Wait>
 __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                             const CUtensorMap& tm_v, const PagedAttend& a, const Plan& pl,
                                             const Tiling& tl, Wait wwait) {
-    const PagedGeom& g = a.g;
     const int lane = threadIdx.x & 31;
-    const int no_abort = 0;
     auto arrive1 = [&](uint64_t* bar) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(bar));
     };
     ptx::tma_prefetch_desc(&tm_q);
     ptx::tma_prefetch_desc(&tm_k);
-    ptx::tma_prefetch_desc(&tm_v);
+    if (with_v) ptx::tma_prefetch_desc(&tm_v);
+    Loader<kCodes, S> ld{sm, a, tm_q, tm_k, tm_v};
     Cursor cur = pl.first;
-    const int page_tokens = 1 << g.page_log2;
-    const int pb_log2 = page_tokens < kKB ? 7 - g.page_log2 : 0;      // pages of a block
-    const int per_block = 1 << pb_log2;
-    const int absent = g.pages * g.Hk;                                // reads as zeros
-    const int batch_log2 = 5 - pb_log2;  // blocks whose pages 32 lanes look up at once
-    int kn = 0, vn = 0, qn = 0, tails = 0;
     bool ok = true, more = pl.u1 > pl.u0;
     for (int si = 0; ok; ++si) {
         const int slot = si % kDescs;
@@ -191,130 +362,34 @@ __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, cons
         }
         const Piece pc = piece_at<kKB>(a.mask, sm.plan, pl, cur, tl);
         const bool pair = pc.n > tl.half;
-        const int at0 = pc.q.total - pc.q.n + pc.i0;
-        if (lane == 0)
-            sm.desc[slot] = Desc{0,          cur.s,        cur.h,        pc.q.q0 + pc.i0, pc.n, at0,
-                                 pc.q.total, pc.blocks.ns, pc.blocks.w0, pc.b0,           pc.b1, pair,
-                                 pc.c0,      pc.c1,        cur.base};
+        const Desc d{0,          cur.s,        cur.h,        pc.q.q0 + pc.i0, pc.n,  pc.q.total - pc.q.n + pc.i0,
+                     pc.q.total, pc.blocks.ns, pc.blocks.w0, pc.b0,           pc.b1, pair,
+                     pc.c0,      pc.c1,        cur.base};
+        if (lane == 0) sm.desc[slot] = d;
         arrive1(&sm.d_full[slot]);
         const int n = pc.b1 - pc.b0;
         if (n > 0) {
-            for (int t = 0; ok && t < (pair ? 2 : 1); ++t, ++qn) {
-                const int qs = qn & 1;
-                if (qn >= 2 && !wwait(&sm.q_empty[qs], ((qn >> 1) - 1) & 1)) {
-                    ok = false;
-                    break;
+            ok = ld.load_q(d, tl.half, wwait);
+            Places at(a, d);
+            if (with_v) {
+                // in the order in which the products give the slots back
+                const int lead = pair ? S::kK - 1 : S::kK;
+                for (int j = 0; ok && j < lead && j < n; ++j) ok = ld.load_k(at, j, wwait);
+                for (int j = 0; ok && j < n; ++j) {
+                    ok = ld.load_v(at, j, wwait);
+                    if (ok && j + lead < n) ok = ld.load_k(at, j + lead, wwait);
+                    at.done(j);
                 }
-                const uint32_t bar = ptx::smem_u32(sm.q_landed(qs));
-                const uint32_t dst = ptx::smem_u32(sm.q[qs]);
-                ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)(tl.half * g.G) * 256u);
-                const int row = pc.q.q0 + pc.i0 + t * tl.half;
-                ptx::tma_load_4d_w(dst, &tm_q, 0, cur.h * g.G, row, 0, bar);
-                ptx::tma_load_4d_w(dst + S::kQHalf, &tm_q, 64, cur.h * g.G, row, 0, bar);
-            }
-            // keys that some query of the tile sees: [0, see_sink) and [see_lo, see_end)
-            const Sight last = sight(a.mask, at0 + pc.n - 1, pc.q.total);
-            const int see_lo = sight(a.mask, at0 < 0 ? 0 : at0, pc.q.total).lo;
-            // Places in the pool (page x heads + head, or absent) of a batch of
-            // blocks, one page per lane; a batch is looked up two batches
-            // before it is needed, so nobody waits for the page table.
-            const int span = page_tokens < kKB ? page_tokens : kKB;
-            auto look_up = [&](int b, uint32_t& needed) -> int {
-                const int j = (b << batch_log2) + (lane >> pb_log2);
-                const int k0 = pc.blocks.at(pc.b0 + j) * kKB + ((lane & (per_block - 1)) << g.page_log2);
-                const bool need = j < n && k0 < last.end && (k0 + span > see_lo || k0 < last.sink);
-                needed = __ballot_sync(0xffffffffu, need);
-                return need ? a.seqs.table[(size_t)cur.s * a.seqs.max_pages + (k0 >> g.page_log2)] : 0;
-            };
-            uint32_t n0, n1, n2;
-            int b0 = look_up(0, n0), b1 = look_up(1, n1), b2 = look_up(2, n2), b_at = 0;
-            // this lane's place of block j, in batch b_at or the next one
-            auto place_of = [&](int j) -> int {
-                const bool later = (j >> batch_log2) > b_at;
-                const int src = ((j << pb_log2) & 31) + (lane & (per_block - 1));
-                const int page = __shfl_sync(0xffffffffu, later ? b1 : b0, src);
-                if (lane >= per_block || !(((later ? n1 : n0) >> src) & 1u)) return absent;
-                if ((unsigned)page < (unsigned)g.pages) return page * g.Hk + cur.h;
-                report(a.err, kErrPagedTable);
-                return absent;
-            };
-            auto load_k = [&](int j) -> bool {
-                const int s = kn % S::kK;
-                const int place = place_of(j);
-                if (kn >= S::kK && !wwait(&sm.k_empty[s], (kn / S::kK - 1) & 1)) return false;
-                const int slot0 = pc.blocks.at(pc.b0 + j) * kKB & (page_tokens - 1);
-                const uint32_t bar = ptx::smem_u32(&sm.k_full[s]);
-                ptx::mbar_arrive_expect_tx_w(bar, (uint32_t)S::kKBytes);
-                if constexpr (kCodes) {
-                    // the scales: 16 bytes per lane and tensor (bulk copies of a
-                    // page's scales cost the copy engine as much as its codes:
-                    // 236 against 191 us without them at 64 streams of 8256 keys)
-                    const int of = ((4 * lane) >> g.page_log2) & (per_block - 1);
-                    const int there = __shfl_sync(0xffffffffu, place, of);
-                    const size_t row = there == absent ? 0 : ((size_t)there << g.page_log2) + slot0 + 4 * lane - (of << g.page_log2);
-                    const uint32_t bytes = there == absent ? 0u : 16u;  // (absent: zeros, as the codes will be)
-                    ptx::cp_async16(ptx::smem_u32(sm.ks(kn) + 4 * lane), a.pool.ks + row, bytes);
-                    ptx::cp_async16(ptx::smem_u32(sm.vs(kn) + 4 * lane), a.pool.vs + row, bytes);
-                    ptx::cp_async_arrive(bar);
-                }
-                __syncwarp();
-                if (lane < per_block) {
-                    const uint32_t dst = ptx::smem_u32(sm.k[s]) + (uint32_t)(lane << g.page_log2) * 128u;
-                    ptx::tma_load_4d(dst, &tm_k, 0, slot0, place, 0, bar);
-                    if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_k, 64, slot0, place, 0, bar);
-                }
-                __syncwarp();
-                ++kn;
-                return true;
-            };
-            auto load_v = [&](int j) -> bool {
-                const int s = vn % S::kVLoads;
-                const int place = place_of(j);
-                if (vn >= S::kVLoads && !wwait(sm.v_taken(s), (vn / S::kVLoads - 1) & 1)) return false;
-                const int key0 = pc.blocks.at(pc.b0 + j) * kKB;
-                const int slot0 = key0 & (page_tokens - 1);
-                uint64_t* full = sm.v_landed(s);
-                if (S::kClearTail && j == n - 1 && key0 + kKB > pc.q.total) {
-                    full = &sm.v_tail;  // a warp of its own clears the tail and hands it on
-                    ++tails;
-                }
-                const uint32_t bar = ptx::smem_u32(full);
-                ptx::mbar_arrive_expect_tx_w(bar, kCodes ? kCodeTile : kTileBytes);
-                __syncwarp();
-                if (lane < per_block) {
-                    const uint32_t dst = ptx::smem_u32(sm.v_load(s)) + (uint32_t)(lane << g.page_log2) * 128u;
-                    ptx::tma_load_4d(dst, &tm_v, 0, slot0, place, 0, bar);
-                    if (!kCodes) ptx::tma_load_4d(dst + kHalfBytes, &tm_v, 64, slot0, place, 0, bar);
-                }
-                __syncwarp();
-                ++vn;
-                return true;
-            };
-            // in the order in which the products give the slots back
-            const int lead = pair ? S::kK - 1 : S::kK;
-            for (int j = 0; ok && j < lead && j < n; ++j) ok = load_k(j);
-            for (int j = 0; ok && j < n; ++j) {
-                ok = load_v(j);
-                if (ok && j + lead < n) ok = load_k(j + lead);
-                if (((j + 1) & ((1 << batch_log2) - 1)) == 0) {
-                    b0 = b1, n0 = n1;
-                    b1 = b2, n1 = n2;
-                    ++b_at;
-                    b2 = look_up(b_at + 2, n2);
+            } else {
+                for (int j = 0; ok && j < n; ++j) {
+                    ok = ld.load_k(at, j, wwait);
+                    at.done(j);
                 }
             }
         }
         more = advance(sm.plan, pl, a.seqs, tl, pc.units, cur);
     }
-            // the last loads of each ring have landed before exit
-    auto landed = [&](uint64_t* bar, int use) {
-        ptx::mbar_wait_bounded(ptx::smem_u32(bar), use & 1, &no_abort, kWaitLimitNs);
-    };
-    for (int i = kn > S::kK ? kn - S::kK : 0; i < kn; ++i) landed(&sm.k_full[i % S::kK], i / S::kK);
-    if (tails) landed(&sm.v_tail, tails - 1);
-    for (int i = vn > S::kVLoads ? vn - S::kVLoads : 0; i < vn; ++i)
-        landed(sm.v_landed(i % S::kVLoads), i / S::kVLoads);
-    for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i) landed(sm.q_landed(i & 1), i >> 1);
+    ld.drain();
     return ok;
 }
 

@@ -482,6 +482,31 @@ def test_many_sequences():
     check_attend(ref.Case(lens, 2, 1, seed=71, page=16))
 
 
+@pytest.mark.parametrize("store", ["native", "e4m3"])
+@pytest.mark.parametrize("max_ctas", [1, 3])
+@pytest.mark.parametrize("new", [1, 20])
+def test_many_short_sequences_on_few_ctas(store, max_ctas, new):
+    """One ragged block after the other through the same rings, the slots
+    behind each sequence's end holding NaN."""
+    lens = [(min(new, t), t) for t in (1 + (i * 29) % 140 for i in range(60))]
+    case = ref.Case(lens, 2, 2, store=store, seed=79, page=16)
+    want = check_attend(case, max_ctas=max_ctas)
+    used = torch.zeros(case.pages, case.page, dtype=torch.bool)
+    for s, (_, t) in enumerate(lens):
+        for j in range(t):
+            used[int(case.table[s, j // case.page]), j % case.page] = True
+    cache = make(case, max_ctas=max_ctas)
+    for p, sl in (~used).nonzero():
+        for x, sc in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
+            if store == "e4m3":
+                x[0, p, :, sl].view(torch.uint8).fill_(0x7f)
+                sc[0, p, :, sl] = float("nan")
+            else:
+                x[0, p, :, sl] = float("nan")
+    assert (cache.attend(case.q.cuda(), batch_of(case)).double().cpu().numpy() == want).all()
+    assert cache.device_status() == 0
+
+
 def test_pool_past_four_gigabytes():
     """Rows whose offsets need more than 32 bits."""
     pages, page = 80000, 128  # 2 heads x 128 tokens x 128 features: 2.6e9 elements, 5.2 GB of keys
