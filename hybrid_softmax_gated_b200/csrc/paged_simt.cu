@@ -75,12 +75,16 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
         float4 o[RM][2];
 #pragma unroll
         for (int i = 0; i < RM; ++i) o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int at0 = pc.q.total - pc.q.n + pc.i0;
+        const paged::Sight hi = paged::sight(a.mask, at0 + pc.n - 1, pc.q.total);
+        const int lo = paged::sight(a.mask, at0 < 0 ? 0 : at0, pc.q.total).lo;
         for (int bi = pc.b0; bi < pc.b1; ++bi) {
             const int key0 = pc.blocks.at(bi) * kKB;
             __syncthreads();
             if (tid < kKB) {
                 long long row = -1;
-                if (key0 + tid < pc.q.total)
+                const int key = key0 + tid;  // (a page that no query of the tile sees is not looked up)
+                if (key < hi.end && (key >= lo || key < hi.sink))
                     row = (long long)paged::pool_row(g, paged::page_at(a.seqs, g, cur.s, key0 + tid, a.err), cur.h,
                                                      key0 + tid);
                 sm.row[tid] = row;

@@ -423,7 +423,8 @@ void arl2_rotary_destroy(arl2_rotary* r);
  *   scale = max(max|x| / 448, 2^-126),  code = e4m3(x * (1 / scale))
  * in fp32, codes rounded to nearest even; a row reads back as code * scale.
  * A row that holds an infinity or NaN gets scale NaN and codes 0: it reads
- * back as NaN.
+ * back as NaN.  (The NaN codes 0x7f and 0xff are never written; in a pool that
+ * the caller filled they must not be in rows that a query sees.)
  *
  * A batch names, for each of its sequences, the chunk of new tokens and the
  * length with them; they are the sequence's last ones.  Row i of sequence s's
@@ -484,7 +485,7 @@ typedef struct {
                               <= 2^30                                         */
     int max_new;           /* the largest number of new tokens of a sequence,
                               or 0 if unknown: which kernel runs depends on
-                              it, no result does                              */
+                              it, results only within their rounding          */
     const int* q_offsets;  /* device int32 [seqs + 1], ascending              */
     const int* kv_lens;    /* device int32 [seqs]                             */
     const int* page_table; /* device int32 [seqs][max_pages]                  */
@@ -516,9 +517,14 @@ arl2_status arl2_paged_read(arl2_paged_handle* h, const arl2_paged_pool* pool, i
  * q_stride elements apart, 0 for dense), over their sequences' keys; query
  * head i reads key head i / (Hq / Hk).  out: [tokens][q_heads][d], dense, not
  * overlapping q or the pool.  block >= 1, window >= 0, sinks >= 0 (see
- * above).  With bf16 the softmax weights are rounded to bf16 before the
- * product with v (times the key's scale, in E4M3), sums and statistics are
- * fp32.  One launch. */
+ * above).  Scores, statistics and sums are fp32.  The tensor-core kernels round
+ * the softmax weights (times the value's scale, in E4M3) before the product
+ * with v: to bf16, or, for at most 16 query rows of a key head and E4M3, to 12
+ * bits; with E4M3 they take q to within 2^-17 of its row's largest element.
+ * Pages none of whose keys a query of the chunk sees are not looked up (a
+ * rolling cache may have given them away).  A key that is not finite and that
+ * only some queries of the same 128 see costs those queries' rows a slow second
+ * computation.  One launch. */
 arl2_status arl2_paged_attend(arl2_paged_handle* h, const arl2_paged_pool* pool, const arl2_paged_batch* batch,
                               int block, int window, int sinks, const void* q, long long q_stride, void* out,
                               cudaStream_t stream);

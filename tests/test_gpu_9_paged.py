@@ -482,6 +482,65 @@ def test_many_sequences():
     check_attend(ref.Case(lens, 2, 1, seed=71, page=16))
 
 
+@pytest.mark.parametrize("dtype,store,impl,d", FORMS)
+@pytest.mark.parametrize("new", [1, 30])
+def test_pages_behind_the_window_may_be_gone(dtype, store, impl, d, new):
+    """Pages that no query of the chunk sees are not looked up."""
+    case = ref.Case([(new, 700), (new, 90)], 2, 2, d=d, dtype=dtype, store=store, seed=83, page=16)
+    want = check_attend(case, impl, window=100, sinks=20)
+    keep = case.table.clone()
+    first = 700 - new + 1 - 100  # first key of the first query's window
+    keep[0, 2:first // 16] = -1  # (the sinks are in pages 0 and 1)
+    cache = make(case, impl)
+    b = PagedBatch(case.q_offsets.cuda(), case.kv_lens.cuda(), keep.cuda(), max_new=new)
+    got = cache.attend(case.q.cuda(), b, window=100, sinks=20)
+    assert cache.device_status() == 0 and (got.double().cpu().numpy() == want).all()
+
+
+def test_batches_without_a_largest_chunk():
+    """max_new unknown: single tokens take the few-row kernel all the same."""
+    case = ref.Case([(1, 1 + 37 * i) for i in range(30)], 8, 2, seed=89)
+    assert (check_attend(case, max_new=0) == check_attend(case, max_new=1)).all()
+
+
+def test_two_handles_at_once_on_two_streams():
+    """Each handle has its own workspace: cut tiles of both in flight together."""
+    cases = [ref.Case([(1, 3000), (1, 2500)], 4, 1, seed=97, page=64), ref.Case([(200, 2500)], 4, 4, seed=101, page=64)]
+    caches, batches = [make(c) for c in cases], [batch_of(c) for c in cases]
+    qs = [c.q.cuda() for c in cases]
+    want = [c.attend(q, b) for c, q, b in zip(caches, qs, batches)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append(caches[i].attend(qs[i], batches[i], stream=s))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
+
+
+@pytest.mark.parametrize("store", ["native", "e4m3"])
+@pytest.mark.parametrize("maker", ["zeros", "tiny", "huge", "mixed"])
+def test_extreme_rows(store, maker):
+    """Value rows of zeros, of 1e-30 and of 1e30 beside ordinary ones, and
+    queries of the same kinds."""
+    case = ref.Case([(1, 300), (40, 200), (3, 60)], 4, 2, store=store, seed=103, page=32)
+    gain = {"zeros": 0.0, "tiny": 1e-30, "huge": 1e25, "mixed": None}[maker]
+    g = torch.Generator().manual_seed(107)
+    x = torch.randn(case.vp.shape, generator=g)
+    each = torch.rand(x.shape[:3], generator=g)
+    rows = torch.where(each < 0.3, torch.tensor(0.0 if gain is None else gain),
+                       torch.where(each < 0.5, torch.tensor(1e-12 if gain is None else 1.0), torch.tensor(1.0)))
+    x = x * rows[..., None]
+    case.vp, case.vs = ref.quantise(x) if store == "e4m3" else (x.to(BF16), None)
+    case.q[0] *= 0.0
+    case.q[1] *= 1e-20
+    case.q[2, :, ::2] *= 1e-4  # elements far below their row's largest
+    check_attend(case)
+    check_attend(case, window=64, sinks=5)
+
+
 @pytest.mark.parametrize("store", ["native", "e4m3"])
 @pytest.mark.parametrize("max_ctas", [1, 3])
 @pytest.mark.parametrize("new", [1, 20])
