@@ -4,7 +4,7 @@
 #pragma once
 
 #include "paged.cuh"
-#include "ptx.cuh"
+#include "ptx_paged.cuh"
 #include "tma.h"
 
 namespace arl2 {

@@ -102,18 +102,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
-// Asynchronous copy of 16 bytes into shared memory (src_bytes = 0: zeros), and an
-// arrival on bar when the thread's copies so far have landed (it counts as one
-// of the barrier's expected arrivals).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(src_bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // 4-D tiled store from this CTA's shared memory (bulk async-group).  Rows
 // outside the tensor are not written.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, uint32_t src, int c0, int c1,
@@ -189,17 +177,6 @@ __device__ __forceinline__ void umma_f16_ss_w(uint32_t d_tmem, uint64_t adesc, u
         "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// The same with e4m3 operands, 32 deep.
-__device__ __forceinline__ void umma_e4m3_ss_w(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -314,15 +291,6 @@ __device__ __forceinline__ void tmem_st32_u(uint32_t taddr, const uint32_t* r) {
         "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -484,13 +452,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
            | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A and B, both K-major, fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-    return (1u << 4)                      // D format fp32 (A and B formats 0: e4m3)
-           | ((uint32_t)(N >> 3) << 17)   // N / 8
-           | ((uint32_t)(M >> 4) << 24);  // M / 16
-}
-
 // Operand tiles of 128 rows x 128 bf16, stored as two 128-row x 64-column
 // halves of 16 KB with the 128-byte swizzle (the layout TMA writes for a
 // {64, ..., 128} box).
@@ -544,36 +505,6 @@ __device__ __forceinline__ void umma_ss8_kk(uint32_t d_tmem, uint64_t a0, uint64
         "add.u32 x, %1, 1030;\n\tadd.u32 y, %3, 1030;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, one;\n\t}" ::"r"(d_tmem),
         "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc0)
-        : "memory");
-}
-// D = A_0 B + A_1 B with e4m3 operands, 128 deep (four k-steps of 32 bytes
-// each): A_0 and A_1 are two K-major tiles of 128 rows x 128 bytes, 16 KB
-// apart, B one such tile.
-__device__ __forceinline__ void umma_e4m3_two_terms(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc) {
-    const uint32_t alo = (uint32_t)a0, ahi = (uint32_t)(a0 >> 32);
-    const uint32_t blo = (uint32_t)b0, bhi = (uint32_t)(b0 >> 32);
-    asm volatile(
-        "{\n\t.reg .pred e, p, one;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
-        "setp.ne.b32 p, %5, %5;\n\t"
-        "setp.eq.b32 one, %5, %5;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t"
-        "add.u32 x, %1, 2;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
-        "add.u32 x, %1, 4;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
-        "add.u32 x, %1, 6;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
-        "add.u32 x, %1, 1024;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
-        "add.u32 x, %1, 1026;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
-        "add.u32 x, %1, 1028;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t"
-        "add.u32 x, %1, 1030;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, one;\n\t}" ::"r"(d_tmem),
-        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc)
         : "memory");
 }
 // A from TMEM (a_tmem, 8 columns of bf16 pairs per k-step), B MN-major:
