@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // O_w += P V in two halves of 64 keys, the last 64 first: they
                 // run while the softmax warps work on the other half's P
                 ptx::umma_ts4_mn(o_t, p_t + 32u, ptx::mnmajor_desc(v_s, 4), idesc_pv, i >= 2 ? 1u : 0u);
-                if (!kCodes) ptx::umma_commit_w(ptx::smem_u32(&sm.pv_half[w]));
+                ptx::umma_commit_w(ptx::smem_u32(&sm.pv_half[w]));
                 const bool next = i + 2 < N;
                 ok = (!next || s_ready(i + 2)) && wwait(&sm.p_full[w], par);
                 if (!ok) break;
@@ -453,7 +453,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 busy = __any_sync(0xffffffffu, r.valid);
             }
             float m_run = -INFINITY, l_run = 0.f;
-            float row_mul = scale_log2;  // scores -> log2 units (codes: with the row's own factor)
+            const float row_mul = scale_log2;  // scores -> log2 units
+            // Codes: a thread has four rows (lane / 4 + 8 r of the warp's 32) and a
+            // quarter of the columns, so that it needs a quarter of the scales: as
+            // one row a thread, their broadcast loads and the products' operands
+            // wait for each other at the shared memory.
+            float qm[4], ql[4], qmul[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                qm[r] = -INFINITY;
+                ql[r] = 0.f;
+                qmul[r] = 0.f;
+            }
             const int step = pair ? 1 : 2, j0 = pair ? 0 : wg;
             for (int j = j0; j < n; j += step) {
                 ok = wwait(&sm.s_full[wg], s_par);
@@ -469,7 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = d.key0(j);
                 const float* kscale = sm.ks(blk + j);
                 const float* vscale = kscale + kKB;
-                if (kCodes && j == j0) row_mul = sm.row_scale[(qn + (pair ? wg : 0)) & 3][row];
+                if (kCodes && j == j0) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        qmul[r] = sm.row_scale[(qn + (pair ? wg : 0)) & 3][(warp & 3) * 32 + (lane >> 2) + 8 * r];
+                }
                 // nothing of the block is hidden from this row
                 const bool open = key0 + kKB <= see.end && (key0 >= see.lo || key0 + kKB <= see.sink);
                 const bool masked = __any_sync(0xffffffffu, !open);
@@ -497,22 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_wait_st();
                 }
                 if (kCodes && masked) kscale = sm.ones;  // (they are scaled already)
-                // columns 32 c .. 32 c + 31 of the scores (codes: times the key scales)
-                auto scaled = [&](uint32_t(&y)[32], int c) {
-                    ptx::reg_fence(y);
-                    if constexpr (kCodes) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(kscale + 32 * c + 4 * i);
-                            const float2 lo = ptx::mul2(make_float2(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])),
-                                                        make_float2(k4.x, k4.y));
-                            const float2 hi = ptx::mul2(make_float2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])),
-                                                        make_float2(k4.z, k4.w));
-                            y[4 * i] = __float_as_uint(lo.x), y[4 * i + 1] = __float_as_uint(lo.y);
-                            y[4 * i + 2] = __float_as_uint(hi.x), y[4 * i + 3] = __float_as_uint(hi.y);
-                        }
-                    }
-                };
                 auto top = [](const uint32_t(&y)[32]) {  // 3-input max tree
                     float m8[4];
 #pragma unroll
@@ -525,35 +524,122 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The weights' base: the running maximum, which moves only when
                 // a half block's scores pass it by more than 2^8.  A warp that
                 // has such a row rescales O_w and the sums.
+                auto rescale_o = [&](float corr) {
+#pragma unroll 1
+                    for (int b = 0; b < 8; ++b) {
+                        uint32_t o[16];
+                        ptx::tmem_ld16(obuf + (uint32_t)b * 16, o);
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence16(o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                        ptx::tmem_st16(obuf + (uint32_t)b * 16, o);
+                    }
+                };
+                // P is handed to the issuer in two halves of 64 keys, the last 64
+                // first, each half's maximum taken just before its weights: the
+                // first products start early (a frame over 24 frames: 422 us,
+                // against 437 with the maximum of all first).
+                if constexpr (kCodes) {
+                    const int q2 = 2 * (lane & 3);
+                    auto half_block = [&](int h, bool has_o) -> bool {  // keys 64 h ..
+                        uint32_t y[2][32];  // lanes 0-15 (rows r = 0, 1), 16-31 (rows 2, 3)
+                        ptx::tmem_ld_quads(sbuf + 64u * h, y[0]);
+                        ptx::tmem_ld_quads(sbuf + (16u << 16) + 64u * h, y[1]);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        ptx::tmem_wait_ld();
+                        ptx::reg_fence(y[0]);
+                        ptx::reg_fence(y[1]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 k2 = *reinterpret_cast<const float2*>(kscale + 64 * h + 8 * i + q2);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                uint32_t &a0 = y[r >> 1][4 * i + 2 * (r & 1)], &a1 = y[r >> 1][4 * i + 2 * (r & 1) + 1];
+                                const float2 x = ptx::mul2(make_float2(__uint_as_float(a0), __uint_as_float(a1)), k2);
+                                a0 = __float_as_uint(x.x), a1 = __float_as_uint(x.y);
+                                mx[r] = ptx::max3(mx[r], x.x, x.y);
+                            }
+                        }
+                        bool need = false;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) * qmul[r];
+                            need = need || mx[r] > qm[r] + kRescaleLog2;
+                        }
+                        if (__any_sync(0xffffffffu, need)) {
+                            float mine = 1.f;  // of the row of O_w that is this lane's
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const bool moves = mx[r] > qm[r] + kRescaleLog2;
+                                const float corr = moves ? ptx::ex2(qm[r] - mx[r]) : 1.f;
+                                qm[r] = moves ? mx[r] : qm[r];
+                                ql[r] *= corr;
+                                const float c = __shfl_sync(0xffffffffu, corr, (lane & 7) * 4);
+                                mine = (lane >> 3) == r ? c : mine;
+                            }
+                            if (has_o) {
+                                if (h == 0) {  // the other half's P V must be in O_w
+                                    if (!wwait(&sm.pv_half[wg], it & 1)) return false;
+                                    ptx::tc_fence_after();
+                                }
+                                rescale_o(mine);
+                            }
+                        }
+                        uint32_t pk[2][16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 v2 = *reinterpret_cast<const float2*>(vscale + 64 * h + 8 * i + q2);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float base = qm[r] == -INFINITY ? 0.f : qm[r];  // nothing seen yet: weights 2^-inf
+                                const float2 x = make_float2(__uint_as_float(y[r >> 1][4 * i + 2 * (r & 1)]),
+                                                             __uint_as_float(y[r >> 1][4 * i + 2 * (r & 1) + 1]));
+                                const float2 e = ptx::fma2(x, make_float2(qmul[r], qmul[r]), make_float2(-base, -base));
+                                const float2 p = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+                                ql[r] += p.x + p.y;
+                                float2 w = ptx::mul2(p, v2);
+                                if (masked) {  // (a hidden value's scale may be anything)
+                                    w.x = p.x == 0.f ? 0.f : w.x;
+                                    w.y = p.y == 0.f ? 0.f : w.y;
+                                }
+                                pk[r >> 1][2 * i + (r & 1)] = ptx::pack_bf16x2(w.x, w.y);
+                            }
+                        }
+                        // (behind the scores that are still to be read)
+                        ptx::tmem_st_quads(sbuf + 64u + 32u * h, pk[0]);
+                        ptx::tmem_st_quads(sbuf + (16u << 16) + 64u + 32u * h, pk[1]);
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        return true;
+                    };
+                    ok = half_block(1, j > j0);
+                    arrive1(&sm.p_half[wg]);
+                    ok = ok && half_block(0, true);
+                    if (!ok) break;
+                    arrive1(&sm.p_full[wg]);
+                    ++it;
+                    continue;
+                }
                 float2 nm;
                 auto set_base = [&]() {
                     const float base = m_run == -INFINITY ? 0.f : m_run;  // nothing seen yet: weights 2^-inf
                     nm = make_float2(-base, -base);
                 };
+                auto over = [&](float mx) { return __any_sync(0xffffffffu, mx > m_run + kRescaleLog2); };
                 auto move_base = [&](float mx, bool has_o) {
                     const bool need = mx > m_run + kRescaleLog2;
                     const float corr = need ? ptx::ex2(m_run - mx) : 1.f;
                     l_run *= corr;
                     m_run = need ? mx : m_run;
-                    if (has_o) {
-#pragma unroll 1
-                        for (int b = 0; b < 8; ++b) {
-                            uint32_t o[16];
-                            ptx::tmem_ld16(obuf + (uint32_t)b * 16, o);
-                            ptx::tmem_wait_ld();
-                            ptx::reg_fence16(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-                            ptx::tmem_st16(obuf + (uint32_t)b * 16, o);
-                        }
-                    }
+                    if (has_o) rescale_o(corr);
                 };
                 // columns 32 c ... -> P, bf16 pairs in columns 64 + 16 c ... of the
                 // buffer (behind the scores that are still to be loaded again)
                 auto weigh = [&](const uint32_t(&y)[32], int c) {
                     uint32_t pk[16];
                     float2 sum4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-                    float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 xi = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
@@ -562,93 +648,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p.x = ptx::ex2(e.x);
                         p.y = ptx::ex2(e.y);
                         sum4[i & 3] = ptx::add2(sum4[i & 3], p);
-                        if constexpr (kCodes) {
-                            // (a hidden value's scale may be anything)
-                            if (i % 2 == 0) v4 = *reinterpret_cast<const float4*>(vscale + 32 * c + 2 * i);
-                            float2 w = ptx::mul2(p, i % 2 == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-                            if (masked) {
-                                w.x = p.x == 0.f ? 0.f : w.x;
-                                w.y = p.y == 0.f ? 0.f : w.y;
-                            }
-                            pk[i] = ptx::pack_bf16x2(w.x, w.y);
-                        } else {
-                            pk[i] = ptx::pack_bf16x2(p.x, p.y);
-                        }
+                        pk[i] = ptx::pack_bf16x2(p.x, p.y);
                     }
                     ptx::tmem_st16(sbuf + 64u + 16u * c, pk);
                     const float2 s2 = ptx::add2(ptx::add2(sum4[0], sum4[1]), ptx::add2(sum4[2], sum4[3]));
                     l_run += s2.x + s2.y;
                 };
-                // P is handed to the issuer in two halves of 64 keys, the last
-                // 64 first.  bf16: each half's maximum just before its weights,
-                // so that the first products start early (a frame over 24
-                // frames: 422 us, against 437 with the maximum of all first).
-                // Codes: the maximum of all first, the first 64 scores loaded
-                // again (two streams' frames: 371 us, against 440 the other
-                // way: the scales' loads then compete with the products'
-                // operands for shared memory).
-                auto over = [&](float mx) { return __any_sync(0xffffffffu, mx > m_run + kRescaleLog2); };
-                if constexpr (kCodes) {
-                    uint32_t ya[32], yb[32], yc[32], yd[32];
-                    ptx::tmem_ld32(sbuf, ya);
-                    ptx::tmem_ld32(sbuf + 32, yb);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_ld32(sbuf + 64, yc);
-                    ptx::tmem_ld32(sbuf + 96, yd);
-                    scaled(ya, 0);
-                    scaled(yb, 1);
-                    float mx = fmaxf(top(ya), top(yb));
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_ld32(sbuf, ya);
-                    scaled(yc, 2);
-                    scaled(yd, 3);
-                    mx = ptx::max3(mx, top(yc), top(yd)) * row_mul;
-                    if (over(mx)) move_base(mx, j > j0);
+                uint32_t ya[32], yb[32];
+                ptx::tmem_ld32(sbuf + 64, ya);
+                ptx::tmem_ld32(sbuf + 96, yb);
+                ptx::tmem_wait_ld();
+                ptx::reg_fence(ya);
+                ptx::reg_fence(yb);
+                float mx = fmaxf(top(ya), top(yb)) * row_mul;
+                // (S of this item was committed after the P V of the previous one: O_w is still)
+                if (over(mx)) move_base(mx, j > j0);
+                set_base();
+                weigh(ya, 2);
+                ptx::tmem_ld32(sbuf, ya);
+                weigh(yb, 3);
+                ptx::tmem_ld32(sbuf + 32, yb);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                arrive1(&sm.p_half[wg]);
+                ptx::tmem_wait_ld();
+                ptx::reg_fence(ya);
+                ptx::reg_fence(yb);
+                mx = fmaxf(top(ya), top(yb)) * row_mul;
+                if (over(mx)) {
+                    ok = wwait(&sm.pv_half[wg], it & 1);  // the first half's P V is in O_w
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    move_base(mx, true);
                     set_base();
-                    weigh(yc, 2);
-                    weigh(yd, 3);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_ld32(sbuf + 32, yb);
-                    scaled(ya, 0);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    arrive1(&sm.p_half[wg]);
-                    weigh(ya, 0);
-                    ptx::tmem_wait_ld();
-                    scaled(yb, 1);
-                    weigh(yb, 1);
-                } else {
-                    uint32_t ya[32], yb[32];
-                    ptx::tmem_ld32(sbuf + 64, ya);
-                    ptx::tmem_ld32(sbuf + 96, yb);
-                    ptx::tmem_wait_ld();
-                    scaled(ya, 2);
-                    scaled(yb, 3);
-                    float mx = fmaxf(top(ya), top(yb)) * row_mul;
-                    // (S of this item was committed after the P V of the previous one: O_w is still)
-                    if (over(mx)) move_base(mx, j > j0);
-                    set_base();
-                    weigh(ya, 2);
-                    ptx::tmem_ld32(sbuf, ya);
-                    weigh(yb, 3);
-                    ptx::tmem_ld32(sbuf + 32, yb);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    arrive1(&sm.p_half[wg]);
-                    ptx::tmem_wait_ld();
-                    scaled(ya, 0);
-                    scaled(yb, 1);
-                    mx = fmaxf(top(ya), top(yb)) * row_mul;
-                    if (over(mx)) {
-                        ok = wwait(&sm.pv_half[wg], it & 1);  // the first half's P V is in O_w
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        move_base(mx, true);
-                        set_base();
-                    }
-                    weigh(ya, 0);
-                    weigh(yb, 1);
                 }
+                weigh(ya, 0);
+                weigh(yb, 1);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 arrive1(&sm.p_full[wg]);
@@ -666,6 +701,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int token = r.token, head = r.head;
             const bool valid = r.valid;
             const bool has[2] = {n > 0, pair ? n > 0 : n > 1};
+            if constexpr (kCodes) {  // to one row a lane
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    ql[r] += __shfl_xor_sync(0xffffffffu, ql[r], 1);
+                    ql[r] += __shfl_xor_sync(0xffffffffu, ql[r], 2);
+                    const float mr = __shfl_sync(0xffffffffu, qm[r], (lane & 7) * 4);
+                    const float lr = __shfl_sync(0xffffffffu, ql[r], (lane & 7) * 4);
+                    m_run = (lane >> 3) == r ? mr : m_run;
+                    l_run = (lane >> 3) == r ? lr : l_run;
+                }
+            }
             // the row's statistics over the piece, and what O_0 and O_1 count
             float m = m_run, l = l_run, f0 = 1.f, f1 = 1.f;
             if (!pair) {
