@@ -26,6 +26,9 @@
 // lazy base c: weights are 2^(score - c), and c moves only when a weight would
 // pass the terms' range, which rescales O.  The two warpgroups take alternate
 // blocks, with their own bases and accumulators; the epilogue combines them.
+// 48 streams of up to 12000 keys (32 heads on 8): 237 us, 6.5 TB/s, the rate of
+// a copy; 64 streams with a window of 8192 keys over e4m3 pages: 183 us, 5.8 TB/s.
+//
 // Schedule, loads and the repair of rows hit by a hidden value that is not
 // finite: paged_tc.cuh.
 #include "paged_tc.cuh"

