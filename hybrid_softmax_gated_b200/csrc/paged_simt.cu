@@ -38,7 +38,22 @@ struct Smem {
     paged::PlanSmem plan;
 };
 
-template <typename T, typename C, int RM>
+// Four consecutive elements.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const __nv_fp8_e4m3* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u, __NV_E4M3)));
+    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> 16), __NV_E4M3)));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// kVec: heads, strides and pointers take four elements at a time.
+template <typename T, typename C, int RM, bool kVec>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, float scale_log2) {
     constexpr int R = 16 * RM;
     constexpr int kPerRow = kThreads / R;  // threads that share a row's statistics
@@ -58,7 +73,17 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
         const paged::Piece pc = paged::piece_at<kKB>(a.mask, sm.plan, pl, cur, tl);
         const int rows = pc.n * g.G;
         __syncthreads();  // the previous tile is done with shared memory
-        for (int i = tid; i < R * 128; i += kThreads) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i0 = 0; i0 < R * 32; i0 += kThreads) {
+                const int r = (i0 + tid) >> 5, c = 4 * ((i0 + tid) & 31), t = r / g.G;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < rows && c < g.d)
+                    x = load4(q + (long long)(pc.q.q0 + pc.i0 + t) * a.q_stride + (cur.h * g.G + r - t * g.G) * g.d + c);
+                *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
+            }
+        }
+        for (int i = kVec ? R * 128 : tid; i < R * 128; i += kThreads) {
             const int r = i >> 7, c = i & 127;
             float x = 0.f;
             if (r < rows && c < g.d)
@@ -94,7 +119,26 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
                 }
             }
             __syncthreads();
-            for (int i = tid; i < kKB * 128; i += kThreads) {
+            if constexpr (kVec) {
+#pragma unroll
+                for (int i0 = 0; i0 < kKB * 32; i0 += kThreads) {
+                    const int j = (i0 + tid) >> 5, c = 4 * ((i0 + tid) & 31);
+                    const long long row = sm.row[j];
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                    if (row >= 0 && c < g.d) {
+                        x = load4(kp + row * g.d + c);
+                        y = load4(vp + row * g.d + c);
+                        if (kCodes) {
+                            const float ks = sm.ks[j], vs = sm.vs[j];
+                            x = make_float4(x.x * ks, x.y * ks, x.z * ks, x.w * ks);
+                            y = make_float4(y.x * vs, y.y * vs, y.z * vs, y.w * vs);
+                        }
+                    }
+                    *reinterpret_cast<float4*>(&sm.k[j][c]) = x;
+                    *reinterpret_cast<float4*>(&sm.v[j][c]) = y;
+                }
+            }
+            for (int i = kVec ? kKB * 128 : tid; i < kKB * 128; i += kThreads) {
                 const int j = i >> 7, c = i & 127;
                 const long long row = sm.row[j];
                 float x = 0.f, y = 0.f;
@@ -273,8 +317,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
     }
 }
 
-template <typename T, typename C, int RM>
-cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
+template <typename T, typename C, int RM, bool kVec>
+cudaError_t launch_as(const PagedAttend& a, int max_ctas, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -283,8 +327,14 @@ cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
     int grid = sms * per_sm;
     static_assert(2 * 16 * 4 <= kPagedRowsPerSm && 2 * 2 * 16 <= kPagedRowsPerSm, "workspace rows");
     if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
-    paged_simt_kernel<T, C, RM><<<grid, kThreads, sizeof(Smem<RM>), st>>>(a, a.scale * 1.4426950408889634f);
+    paged_simt_kernel<T, C, RM, kVec><<<grid, kThreads, sizeof(Smem<RM>), st>>>(a, a.scale * 1.4426950408889634f);
     return cudaGetLastError();
+}
+
+template <typename T, typename C, int RM>
+cudaError_t launch(const PagedAttend& a, int max_ctas, cudaStream_t st) {
+    const bool vec = a.g.d % 4 == 0 && a.q_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.q) % (4 * sizeof(T)) == 0;
+    return vec ? launch_as<T, C, RM, true>(a, max_ctas, st) : launch_as<T, C, RM, false>(a, max_ctas, st);
 }
 
 template <typename T, typename C>
@@ -296,13 +346,17 @@ cudaError_t launch_rows(const PagedAttend& a, int max_new, int max_ctas, cudaStr
     return launch<T, C, 4>(a, max_ctas, st);
 }
 
+template <typename T, typename C, int RM, bool kVec>
+cudaError_t allow() {
+    return cudaFuncSetAttribute(paged_simt_kernel<T, C, RM, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Smem<RM>));
+}
 template <typename T, typename C>
 cudaError_t init_one() {
-    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, C, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(Smem<1>));
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(paged_simt_kernel<T, C, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(Smem<4>));
+    cudaError_t e = allow<T, C, 1, false>();
+    if (e == cudaSuccess) e = allow<T, C, 1, true>();
+    if (e == cudaSuccess) e = allow<T, C, 4, false>();
+    return e == cudaSuccess ? allow<T, C, 4, true>() : e;
 }
 
 }  // namespace
