@@ -10,8 +10,10 @@
 // whatever it holds.  The CTAs split all tiles' blocks evenly and merge a cut
 // tile's partials (paged.cuh).  Bound by the fp32 pipes: per 4 features of
 // the products a thread loads RM + 4 vectors from shared memory for 16 RM
-// multiply-adds.
+// multiply-adds (12 to 16 TFLOP/s on long chunks); short calls by one block's
+// latency, 14 to 25 us.
 #include "paged.cuh"
+#include "ptx.cuh"
 
 #include <cmath>
 #include <type_traits>
@@ -62,6 +64,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
     Smem<RM>& sm = *reinterpret_cast<Smem<RM>*>(smem_raw);
     const PagedGeom& g = a.g;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    ptx::pdl_wait_then_trigger();
     const paged::Tiling tl{R / g.G, R / g.G, 1, 1, 1, 0, 1};
     const paged::Plan pl = paged::make_plan<kKB>(g, a.seqs, a.mask, tl, 1, sm.plan, sm.tiles, a.err);
     if (pl.u1 == pl.u0) return;
@@ -327,8 +330,8 @@ cudaError_t launch_as(const PagedAttend& a, int max_ctas, cudaStream_t st) {
     int grid = sms * per_sm;
     static_assert(2 * 16 * 4 <= kPagedRowsPerSm && 2 * 2 * 16 <= kPagedRowsPerSm, "workspace rows");
     if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
-    paged_simt_kernel<T, C, RM, kVec><<<grid, kThreads, sizeof(Smem<RM>), st>>>(a, a.scale * 1.4426950408889634f);
-    return cudaGetLastError();
+    return launch_pdl(paged_simt_kernel<T, C, RM, kVec>, grid, kThreads, sizeof(Smem<RM>), st, a,
+                      a.scale * 1.4426950408889634f);
 }
 
 template <typename T, typename C, int RM>
@@ -342,7 +345,12 @@ cudaError_t launch_rows(const PagedAttend& a, int max_new, int max_ctas, cudaStr
     // 16-row tiles when that holds every sequence's rows of a key head, or
     // the group alone fills them; 64-row tiles read a key block once for
     // four times the rows
-    if (a.g.G <= 16 && (long long)max_new * a.g.G <= 16) return launch<T, C, 1>(a, max_ctas, st);
+    const long long tiles = ((long long)a.seqs.tokens * a.g.G + 63) / 64 * a.g.Hk;
+    const long long keys = (long long)a.seqs.max_pages << a.g.page_log2;
+    // (also when 64-row tiles would leave most SMs without work: 34 tokens of 8
+    // heads on 43 keys 21 -> 16 us; 160 of 24 on 98 keys would take 33, not 27)
+    if (a.g.G <= 16 && ((long long)max_new * a.g.G <= 16 || tiles * ((keys + kKB - 1) / kKB) <= 74))
+        return launch<T, C, 1>(a, max_ctas, st);
     return launch<T, C, 4>(a, max_ctas, st);
 }
 
