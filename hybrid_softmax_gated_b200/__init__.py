@@ -567,10 +567,12 @@ def _token_stride(t) -> int:
 
 
 def _table(t, name, shape, device):
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or any(
-            w is not None and w != n for w, n in zip(shape, t.shape)):
-        want = ["n" if w is None else w for w in shape]
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {want}")
+    good = t.dtype == torch.int32 and t.device == device and t.is_contiguous() and t.dim() == len(shape)
+    if good:
+        for want, n in zip(shape, t.shape):
+            good = good and (want is None or want == n)
+    if not good:
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {['n' if w is None else w for w in shape]}")
     return t
 
 
@@ -583,7 +585,8 @@ def _used(t, stream):
 
 
 def _like(t, stream):
-    return _used(torch.empty_like(t, memory_format=torch.contiguous_format), stream)
+    t = torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
+    return t if stream is None else _used(t, stream)
 
 
 class RotaryAxes:
@@ -783,7 +786,7 @@ class PagedCache:
         outs = []
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             if t is None:
-                t = _used(torch.empty(shape, dtype=self.dtype, device=self.device), stream)
+                t = _used(page_table.new_empty(shape, dtype=self.dtype), stream)
             elif not self._rows(t, name, 1, tokens).is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
             outs.append(t)
@@ -819,8 +822,7 @@ class PagedCache:
             if positions is None or rotary.head_dim != self.head_dim:
                 raise ValueError("rotary needs positions and the cache's head_dim")
             _table(positions, "positions", (tokens, rotary.axes), self.device)
-            turned = _used(torch.empty((tokens, sum(self.heads), self.head_dim), dtype=self.dtype, device=self.device),
-                           stream)
+            turned = _used(q.new_empty((tokens, sum(self.heads), self.head_dim)), stream)
         out = self._out(out, q, stream)
         _check(_lib.arl2_paged_forward(self.handle, self._pool(layer), self._batch(batch, tokens),
                                        None if rotary is None else rotary.handle,
