@@ -42,7 +42,9 @@ struct Place {
 };
 
 // Writing: row i of a sequence's n is its position total - n + i; reading:
-// starts[s] + i (starts == nullptr: i).  The whole warp.
+// starts[s] + i (starts == nullptr: i).  The whole warp.  owner_of is right for
+// ascending offsets only: among others the row may lie outside the sequence it
+// names, and then it has no position.
 __device__ __forceinline__ Place find_place(const PagedGeom& g, const PagedSeqs& b, const int* starts, bool reading,
                                             int tok, int* err) {
     const int s = owner_of(b.q_off, b.S, tok);
@@ -51,7 +53,7 @@ __device__ __forceinline__ Place find_place(const PagedGeom& g, const PagedSeqs&
     const long long cap = (long long)b.max_pages << g.page_log2;
     const int q0 = b.q_off[s], q1 = b.q_off[s + 1];
     long long at;
-    bool bad = q0 < 0 || q1 < q0 || q1 > b.tokens;
+    bool bad = q0 < 0 || tok < q0 || tok >= q1 || q1 > b.tokens;
     if (reading) {
         at = (long long)(starts ? starts[s] : 0) + (tok - q0);
         bad = bad || at < 0 || at >= cap;

@@ -451,7 +451,9 @@ void arl2_rotary_destroy(arl2_rotary* r);
  * beyond max_pages pages, or a page number outside the pool sets the
  * handle's error word: the sequence (or the page) is skipped, outputs of
  * the sequence are undefined, and arl2_paged_device_status reports
- * INVALID_ARG. */
+ * INVALID_ARG.  With offsets out of order, rows that belong to another
+ * sequence's range as well may be skipped with it, and what they share is
+ * undefined; no row is written to or read from a position other than its own. */
 typedef enum { ARL2_CACHE_NATIVE = 0, ARL2_CACHE_E4M3 = 1 } arl2_cache_format;
 
 typedef struct arl2_paged_handle arl2_paged_handle;
