@@ -74,6 +74,18 @@ __device__ __forceinline__ Place find_place(const PagedGeom& g, const PagedSeqs&
     return pl;
 }
 
+// The grid's last block has no rows: it looks at all sequences' entries, those
+// that no row leads to as well.  (Beside the rows' blocks, it costs them nothing.)
+__device__ __forceinline__ bool check_block(const PagedGeom& g, const PagedSeqs& b, int* err) {
+    if (blockIdx.x + 1 < gridDim.x) return false;
+    const long long cap = (long long)b.max_pages << g.page_log2;
+    for (int s = threadIdx.x; s < b.S; s += kThreads) {
+        const int q0 = b.q_off[s], q1 = b.q_off[s + 1], total = b.kv_len ? b.kv_len[s] : 0;
+        if (q0 < 0 || q1 < q0 || q1 > b.tokens || total < 0 || total > cap) paged::report(err, kErrPagedTable);
+    }
+    return true;
+}
+
 // The warp's share of the tokens' rows (K's heads, then V's): kSteps steps of
 // kPer rows of one token.
 struct Share {
@@ -156,6 +168,7 @@ template <typename T, bool kCodes, int kLanes>
 __global__ void __launch_bounds__(kThreads) write_kernel(PagedGeom g, PagedPool pool, PagedSeqs b, const T* k,
                                                          long long k_stride, const T* v, long long v_stride, int* err) {
     ptx::pdl_wait_then_trigger();
+    if (check_block(g, b, err)) return;
     constexpr int kRow = kLanes ? kLanes : 32, kPer = 32 / kRow;
     const int rows = 2 * g.Hk;
     const Share sh = share_of(rows, kSteps * kPer);
@@ -257,6 +270,7 @@ template <typename T, bool kCodes, int kLanes>
 __global__ void __launch_bounds__(kThreads) read_kernel(PagedGeom g, PagedPool pool, PagedSeqs b, const int* starts,
                                                         T* k, T* v, int* err) {
     ptx::pdl_wait_then_trigger();
+    if (check_block(g, b, err)) return;
     constexpr int kRow = kLanes ? kLanes : 32, kPer = 32 / kRow;
     const int rows = 2 * g.Hk;
     const Share sh = share_of(rows, kSteps * kPer);
@@ -326,10 +340,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(PagedGeom g, PagedPool p
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Blocks for the tokens' rows, `per` rows a step.
+// Blocks for the tokens' rows, `per` rows a step, and the one that checks.
 unsigned blocks_for(int tokens, int Hk, int per) {
     const int parts = (2 * Hk + kSteps * per - 1) / (kSteps * per);
-    return (unsigned)(((long long)tokens * parts + kThreads / 32 - 1) / (kThreads / 32));
+    return (unsigned)(((long long)tokens * parts + kThreads / 32 - 1) / (kThreads / 32) + 1);
 }
 
 template <typename T, bool kCodes>

@@ -28,7 +28,7 @@ def shuffled(seqs, tokens, seed):
 
 @pytest.mark.parametrize("dtype,store,d", [(BF16, "native", 128), (BF16, "e4m3", 128), (FP32, "e4m3", 64), (FP32, "native", 40)])
 @pytest.mark.parametrize("offsets,tokens", [
-    ([0, 100, 1, 2], 64), ([0, 2, 100, 3, 5], 100), ([0, 60, 70, 40], 70), ([0, 60, 70, 40], 100),
+    ([0, 100, 1, 2], 64), ([0, 2, 100, 3, 5], 100), ([0, 60, 70, 40], 70), ([0, 60, 70, 40], 100), ([5, 3, 9, 64], 64),
     (shuffled(40, 90, 1), 90), (shuffled(300, 200, 2), 200),
 ])
 def test_offsets_out_of_order(dtype, store, d, offsets, tokens):
