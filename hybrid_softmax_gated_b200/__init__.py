@@ -576,17 +576,37 @@ def _table(t, name, shape, device):
     return t
 
 
-def _used(t, stream):
-    """t, an output of this call; the allocator is told when it is used on
-    another stream than the current one."""
-    if isinstance(stream, torch.cuda.Stream) and stream != torch.cuda.current_stream(t.device):
-        t.record_stream(stream)
+def _side(stream, device):
+    """The torch stream that a call's `stream` (a Stream, a raw handle, None)
+    stands for, or None if that is the current one."""
+    if stream is None:
+        return None
+    handle = _stream(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _empty(like, shape, dtype, stream):
+    """Memory for a call on `stream`: allocated there, so that it is neither in
+    use by the current stream nor given to it while the call runs; the current
+    stream, where the caller uses it, is recorded."""
+    side = _side(stream, like.device)
+    if side is None:
+        return like.new_empty(shape, dtype=dtype)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(side):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
     return t
 
 
 def _like(t, stream):
-    t = torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
-    return t if stream is None else _used(t, stream)
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(t, t.shape, t.dtype, stream)
 
 
 class RotaryAxes:
@@ -701,6 +721,11 @@ class PagedCache:
     kv_heads, page_tokens, d] in dtype or, with cache_format="e4m3", 8-bit
     codes with k_scales, v_scales fp32 [layers, pages, kv_heads, page_tokens].
     pool: existing ones instead, (k_pages, v_pages, k_scales, v_scales).
+
+    Calls take a stream (a torch stream or a raw handle; default: the current
+    one).  What they return may be used on that stream and, once the caller has
+    made it wait, on the current one; what they are given has to outlive the
+    kernels (record_stream, for a tensor of another stream).
     """
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, pages: int, page_tokens: int, *, layers: int = 1,
@@ -786,7 +811,7 @@ class PagedCache:
         outs = []
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             if t is None:
-                t = _used(page_table.new_empty(shape, dtype=self.dtype), stream)
+                t = _empty(page_table, shape, self.dtype, stream)
             elif not self._rows(t, name, 1, tokens).is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
             outs.append(t)
@@ -822,7 +847,7 @@ class PagedCache:
             if positions is None or rotary.head_dim != self.head_dim:
                 raise ValueError("rotary needs positions and the cache's head_dim")
             _table(positions, "positions", (tokens, rotary.axes), self.device)
-            turned = _used(q.new_empty((tokens, sum(self.heads), self.head_dim)), stream)
+            turned = _empty(q, (tokens, sum(self.heads), self.head_dim), self.dtype, stream)
         out = self._out(out, q, stream)
         _check(_lib.arl2_paged_forward(self.handle, self._pool(layer), self._batch(batch, tokens),
                                        None if rotary is None else rotary.handle,

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import paged_reference as ref
-from hybrid_softmax_gated_b200 import PagedBatch, PagedCache
+from hybrid_softmax_gated_b200 import PagedBatch, PagedCache, RotaryAxes
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,73 @@ def test_offsets_out_of_order(dtype, store, d, offsets, tokens):
             if a < b <= tokens:
                 fine[a:b] |= (got[a:b] == of[s * length:s * length + b - a]).flatten(1).all(1)
         assert fine.all()
+
+
+# ---- streams -----------------------------------------------------------------
+
+def busy(stream, cycles=60_000_000):
+    """Tens of milliseconds of nothing on a stream: what follows there is late."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(cycles)
+
+
+def fill_free_memory(sizes):
+    """Takes what the current stream's allocator has free at these sizes, and
+    writes it."""
+    held = [torch.full((n,), float("nan"), dtype=BF16, device="cuda") for n in sizes for _ in range(8)]
+    torch.cuda.current_stream().synchronize()
+    return held
+
+
+def step_case(store="native", new=40):
+    case = ref.Case([(new, 300), (3, 90)], 4, 2, store=store, seed=11, page=32)
+    cache = PagedCache(4, 2, 128, case.pages, 32, cache_format=store)
+    batch = PagedBatch(case.q_offsets.cuda(), case.kv_lens.cuda(), case.table.cuda(), max_new=new)
+    positions = torch.arange(case.tokens, dtype=torch.int32)[:, None].cuda()
+    return cache, batch, case.q.cuda(), case.k.cuda(), case.v.cuda(), positions
+
+
+@pytest.mark.parametrize("handle", ["stream", "raw"])
+def test_scratch_and_outputs_live_on_the_calls_stream(handle):
+    """What a call allocates for another stream is not given away while that
+    stream still has to use it."""
+    cache, batch, q, k, v, positions = step_case()
+    plan = RotaryAxes(128, [128])
+    want = cache.forward(q, k, v, batch, rotary=plan, positions=positions)
+    turned = plan.apply(q, k, positions)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    on = s if handle == "stream" else s.cuda_stream
+    sizes = [q.shape[0] * (4 + 2) * 128, q.numel(), k.numel()]
+    busy(s)
+    out = cache.forward(q, k, v, batch, rotary=plan, positions=positions, out=torch.empty_like(q), stream=on)
+    held = fill_free_memory(sizes)  # (the scratch was free for the current stream?)
+    s.synchronize()
+    assert torch.equal(out, want)
+    busy(s)
+    plan.apply(q, k, positions, stream=on)  # outputs dropped at once
+    cache.attend(q, batch, stream=on)
+    late = fill_free_memory(sizes)
+    s.synchronize()
+    assert all(torch.isnan(t).all() for t in held + late)
+
+
+@pytest.mark.parametrize("handle", ["stream", "raw"])
+def test_outputs_on_a_side_stream_are_not_memory_in_use(handle):
+    """A block that the current stream has freed but is not done with is no
+    output for another stream."""
+    cache, batch, q, k, v, positions = step_case()
+    plan = RotaryAxes(128, [128])
+    want = [cache.attend(q, batch), *plan.apply(q, k, positions), *cache.read(batch.tensors[2][:1], batch.tensors[0][:2], 40)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    on = s if handle == "stream" else s.cuda_stream
+    old = fill_free_memory([q.numel(), k.numel(), 40 * 2 * 128])
+    busy(torch.cuda.current_stream())
+    for t in old:
+        t.fill_(3.0)
+    del old, t
+    got = [cache.attend(q, batch, stream=on), *plan.apply(q, k, positions, stream=on),
+           *cache.read(batch.tensors[2][:1], batch.tensors[0][:2], 40, stream=on)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
