@@ -733,7 +733,11 @@ class PagedCache:
                  impl: str = "auto", max_ctas: int = 0, pool=None, device=None, stream=None):
         dt = _dtype(dtype)
         e4m3 = {"native": False, "e4m3": True}[cache_format]
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.device = torch.device("cuda" if device is None else device)
+        if self.device.type != "cuda":
+            raise ValueError("device must be a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.heads, self.head_dim, self.dtype, self.layers = (q_heads, kv_heads), head_dim, dtype, layers
         cfg = Arl2PagedConfig(q_heads, kv_heads, head_dim, pages, page_tokens, dt,
                               ARL2_CACHE_E4M3 if e4m3 else ARL2_CACHE_NATIVE, float(softmax_scale),

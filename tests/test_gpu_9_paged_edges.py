@@ -142,3 +142,14 @@ def test_outputs_on_a_side_stream_are_not_memory_in_use(handle):
            *cache.read(batch.tensors[2][:1], batch.tensors[0][:2], 40, stream=on)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_device_without_an_index_is_the_current_one():
+    cache = PagedCache(2, 2, 128, 4, 16, device="cuda")
+    assert cache.device == torch.device("cuda", torch.cuda.current_device()) == cache.k_pages.device
+    k = torch.randn(5, 2, 128, device="cuda").to(BF16)
+    table, offsets = torch.arange(4, dtype=torch.int32)[None].cuda(), torch.tensor([0, 5], dtype=torch.int32).cuda()
+    batch = PagedBatch(offsets, offsets[1:], table)
+    cache.write(k, k, batch)
+    cache.attend(k, batch)
+    assert torch.equal(cache.read(table, offsets, 5)[0], k) and cache.device_status() == 0
