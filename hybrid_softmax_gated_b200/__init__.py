@@ -760,10 +760,16 @@ class PagedCache:
         with torch.cuda.device(self.device):
             _check(_lib.arl2_paged_create(ctypes.byref(cfg), _stream(stream), ctypes.byref(h)), "arl2_paged_create")
         self._h = h
-        if pool is None:
-            k, v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else dtype, device=self.device).view(store)
-                    for _ in range(2))
-            ks, vs = (torch.zeros(shape[:4], device=self.device) if e4m3 else None for _ in range(2))
+        if pool is None:  # (cleared on the given stream, like the handle's own memory)
+            near = torch.empty(0, device=self.device)
+            k, v = (_empty(near, shape, torch.uint8 if e4m3 else dtype, stream) for _ in range(2))
+            ks, vs = (_empty(near, shape[:4], torch.float32, stream) if e4m3 else None for _ in range(2))
+            side = _side(stream, self.device)
+            with torch.cuda.stream(side) if side is not None else torch.cuda.device(self.device):
+                for t in (k, v, ks, vs):
+                    if t is not None:
+                        t.zero_()
+            k, v = k.view(store), v.view(store)
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = k, v, ks, vs
         self._pools = [Arl2PagedPool(k[i].data_ptr(), v[i].data_ptr(), None if ks is None else ks[i].data_ptr(),
                                      None if vs is None else vs[i].data_ptr()) for i in range(layers)]

@@ -144,6 +144,32 @@ def test_outputs_on_a_side_stream_are_not_memory_in_use(handle):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("store", ["native", "e4m3"])
+@pytest.mark.parametrize("handle", ["stream", "raw"])
+def test_a_new_cache_is_cleared_on_its_stream(handle, store):
+    """Pages written right after the cache was made on a busy day of the
+    current stream keep what was written."""
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(64, 2, 128, generator=g).to(BF16).cuda() for _ in range(2))
+    table, offsets = torch.arange(4, dtype=torch.int32)[None].cuda(), torch.tensor([0, 64], dtype=torch.int32).cuda()
+    batch = PagedBatch(offsets, offsets[1:], table)
+    PagedCache(2, 2, 128, 4, 16, cache_format=store).close()  # (memory that the current stream has at hand)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy(torch.cuda.current_stream())
+    on = s if handle == "stream" else s.cuda_stream
+    cache = PagedCache(2, 2, 128, 4, 16, cache_format=store, stream=on)
+    cache.write(k, v, batch, stream=on)
+    s.synchronize()
+    torch.cuda.synchronize()
+    got = cache.read(table, offsets, 64)
+    if store == "native":
+        assert torch.equal(got[0], k) and torch.equal(got[1], v)
+    for x, y in zip(got, (k, v)):  # (a code is off by half a step of 2^-4 at most, and the value is rounded once)
+        tol = (2.0 ** -4 + 2.0 ** -8) * y.float().abs() + 2.0 ** -10 * y.float().abs().amax(-1, keepdim=True) / 448
+        assert ((x.float() - y.float()).abs() <= tol * 1.01).all()
+
+
 def test_a_device_without_an_index_is_the_current_one():
     cache = PagedCache(2, 2, 128, 4, 16, device="cuda")
     assert cache.device == torch.device("cuda", torch.cuda.current_device()) == cache.k_pages.device
