@@ -714,6 +714,21 @@ class PagedBatch:
         return ctypes.byref(c)
 
 
+def _check_pool(pool, shape, store, e4m3):
+    """A given pool (k_pages, v_pages, k_scales, v_scales), all on one device."""
+    k, v, ks, vs = pool
+    for t, name, want, sh in ((k, "k_pages", store, shape), (v, "v_pages", store, shape),
+                              (ks, "k_scales", torch.float32, shape[:4]), (vs, "v_scales", torch.float32, shape[:4])):
+        if name.endswith("scales") and not e4m3:
+            if t is not None:
+                raise ValueError(f"{name}: this format has none")
+        elif t is None or t.dtype != want or tuple(t.shape) != tuple(sh) or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor {list(sh)} of {want}")
+        elif t.device != k.device:
+            raise ValueError(f"{name} must be on k_pages' device")
+    return k, v, ks, vs
+
+
 class PagedCache:
     """A paged KV cache and the attention that reads it (arl2_paged_*).
 
@@ -745,16 +760,7 @@ class PagedCache:
         shape = (layers, pages, kv_heads, page_tokens, head_dim)
         store = torch.float8_e4m3fn if e4m3 else dtype
         if pool is not None:
-            k, v, ks, vs = pool
-            for t, name, want, sh in ((k, "k_pages", store, shape), (v, "v_pages", store, shape),
-                                      (ks, "k_scales", torch.float32, shape[:4]),
-                                      (vs, "v_scales", torch.float32, shape[:4])):
-                if t is None and not e4m3 and name.endswith("scales"):
-                    continue
-                if t is None or (name.endswith("scales") and not e4m3) or t.dtype != want or tuple(t.shape) != sh \
-                        or not t.is_cuda or not t.is_contiguous():
-                    raise ValueError(f"{name} must be a contiguous CUDA tensor {list(sh)} of {want}"
-                                     if e4m3 or not name.endswith("scales") else f"{name}: this format has none")
+            k, v, ks, vs = _check_pool(pool, shape, store, e4m3)
             self.device = k.device
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):

@@ -1,5 +1,6 @@
 """The paged cache's binding: argument checks that need no GPU."""
 import pytest
+import torch
 
 import hybrid_softmax_gated_b200 as arl2
 
@@ -7,3 +8,43 @@ import hybrid_softmax_gated_b200 as arl2
 def test_the_device_must_be_a_gpu():
     with pytest.raises(ValueError, match="device"):
         arl2.PagedCache(2, 2, 128, 4, 16, device="cpu")
+
+
+class Fake:
+    """What the checks ask of a tensor."""
+
+    def __init__(self, shape, dtype, index=0, contiguous=True):
+        self.shape, self.dtype, self.device, self.is_cuda = shape, dtype, torch.device("cuda", index), True
+        self.is_contiguous = lambda: contiguous
+
+
+SHAPE = (2, 4, 2, 16, 128)
+
+
+def pool(e4m3, **change):
+    store = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kinds = [(SHAPE, store), (SHAPE, store), (SHAPE[:4], torch.float32), (SHAPE[:4], torch.float32)]
+    names = ["k", "v", "ks", "vs"]
+    return tuple(None if n not in ("k", "v") and not e4m3 and n not in change else Fake(*kind, **change.get(n, {}))
+                 for n, kind in zip(names, kinds))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_pool_is_on_one_device(e4m3):
+    store = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    good = pool(e4m3)
+    assert arl2._check_pool(good, SHAPE, store, e4m3) == good
+    moved = {n: dict(index=1) for n in ("k", "v", "ks", "vs")}
+    if e4m3:
+        arl2._check_pool(pool(True, **moved), SHAPE, store, True)  # all on another one
+    for n in ("k", "v", "ks", "vs") if e4m3 else ("k", "v"):
+        with pytest.raises(ValueError, match="device"):
+            arl2._check_pool(pool(e4m3, **{n: dict(index=1)}), SHAPE, store, e4m3)
+        with pytest.raises(ValueError, match="contiguous"):
+            arl2._check_pool(pool(e4m3, **{n: dict(contiguous=False)}), SHAPE, store, e4m3)
+    if e4m3:
+        with pytest.raises(ValueError, match="k_scales"):
+            arl2._check_pool(good[:2] + (None, good[3]), SHAPE, store, True)
+    else:
+        with pytest.raises(ValueError, match="none"):
+            arl2._check_pool(pool(False, vs={}), SHAPE, store, False)
