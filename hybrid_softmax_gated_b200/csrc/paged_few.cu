@@ -29,8 +29,8 @@
 // 48 streams of up to 12000 keys (32 heads on 8): 237 us, 6.5 TB/s, the rate of
 // a copy; 64 streams with a window of 8192 keys over e4m3 pages: 183 us, 5.8 TB/s.
 //
-// Schedule, loads and the repair of rows hit by a hidden value that is not
-// finite: paged_tc.cuh.
+// Schedule, loads and what keeps hidden values that are not finite out of the
+// products: paged_tc.cuh.
 #include "paged_tc.cuh"
 
 #include <cmath>
@@ -68,7 +68,7 @@ struct __align__(1024) Smem {
     static constexpr int kVLoads = kCodes ? 5 : 3;
     static constexpr int kTerms = kCodes ? 3 : 1;
     static constexpr uint32_t kQHalf = kN * 128;
-    static constexpr bool kClearTail = true;
+    static constexpr bool kClean = true;
     uint8_t k[kK][kKBytes];
     uint8_t v[kVLoads][kKBytes];
     uint8_t q[2][2 * kQHalf];                 // two halves of 64 features; codes: then the two terms
@@ -88,7 +88,7 @@ struct __align__(1024) Smem {
     uint64_t q_raw[2], q_full[2], q_empty[2];
     uint64_t k_full[kK], k_empty[kK];
     uint64_t v_full[kVLoads], v_empty[kVLoads];
-    uint64_t v_tail;
+    uint64_t v_edge[kVLoads];  // a block of V that some query does not see all of: landed, not cleaned yet
     uint64_t s_full[4], s_taken[4];  // by item & 3: S in TMEM; read (4 warp arrivals)
     uint64_t p_full[2], pv_done[2];  // by warpgroup: 4 warp arrivals; one commit per item
     uint64_t o_free, ebar, wbar[2], drain;
@@ -114,6 +114,26 @@ __device__ __forceinline__ uint32_t e4m3_of(float x) {
 }
 __device__ __forceinline__ float of_e4m3(uint32_t c) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
+}
+
+// What rows first .. first + 7 of a piece that had values taken out get of them
+// (lane l knows what row l sees): feature `at`.
+static __device__ __noinline__ void give_rows_back(const PagedAttend& a, const Desc& d, paged::Sight mine, int first, int at,
+                                                   float (&sum)[8]) {
+    const paged::Seen seen = paged::seen_by(a.mask, d);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) sum[r] = 0.f;
+    paged::for_edge_keys(a, d, seen, [&](const __nv_bfloat16* v, int j) {
+#pragma unroll 8
+        for (int u = 0; u < paged::kEdgeKeys; ++u) {
+            const float x = __bfloat162float(v[u * kD + at]);
+            const uint32_t rows =
+                __ballot_sync(0xffffffffu, paged::sees(mine, j + u) && !paged::sees(seen.all, j + u)) >> first;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if ((rows >> r & 1u) && !(fabsf(x) < INFINITY)) sum[r] += x;
+        }
+    });
 }
 
 // NR: rows of a tile (4, 8 or 16).
@@ -148,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < S::kVLoads; ++i) {
             init(&sm.v_full[i], 1);
             init(&sm.v_empty[i], 1);
+            init(&sm.v_edge[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             init(&sm.q_raw[i], 1);
@@ -157,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             init(&sm.pv_done[i], 1);
             init(&sm.wbar[i], kWgWarps);
         }
-        init(&sm.v_tail, 1);
         init(&sm.o_free, kSoftmaxWarps);
         init(&sm.ebar, kSoftmaxWarps);
         init(&sm.drain, 1);
@@ -288,29 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_wait_bounded(ptx::smem_u32(&sm.drain), 0, &no_abort, kWaitLimitNs);
         }
     } else if (warp == 2) {
-        // ----------------------------------- slots behind the last key --
-        int vn = 0, tails = 0;
-        bool ok = true;
-        for (int si = 0; ok; ++si) {
-            Desc d;
-            if (!get_desc(si, d)) {
-                ok = false;
-                break;
-            }
-            if (d.done) break;
-            const int n = d.b1 - d.b0;
-            if (n <= 0) continue;
-            vn += n;
-            const int key0 = d.key0(n - 1);
-            if (key0 + kKB <= d.total) continue;
-            ok = wwait(&sm.v_tail, tails & 1);
-            ++tails;
-            if (!ok) break;
-            const int s = (vn - 1) % S::kVLoads;  // the piece's last tile
-            paged::clear_tail(sm.v[s], kCodes ? 1 : 2, key0, d.total);
-            arrive1(&sm.v_full[s]);
-        }
-        if (!ok) fail();
+        // -------------------------- what is hidden in V and not finite --
+        if (!paged::clean_pieces<kCodes>(sm, a.mask, get_desc, wwait)) fail();
     } else if (warp == 3) {
         // ------------------------- V's loader; codes: Q in two terms --
         // (one warp for all loads would take 1560 cycles a block of codes: more
@@ -562,6 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return ((size_t)(d.row0 + token) * g.Hq + d.h * g.G + r - token * g.G) * kD;
             };
             float* part = a.work.o + (size_t)slot * kN * kD;
+            if constexpr (!kCodes) {
+                if (d.taken) {
+                    float back[8];
+                    give_rows_back(a, d, lane < rows ? see : paged::Sight{0, 0, 0}, r0, at, back);
+#pragma unroll
+                    for (int r = 0; r < NR / 2; ++r) acc[r] += back[r];
+                }
+            }
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r) {
                 const int row = r0 + r;
@@ -581,22 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[row * kD + at] = acc[r];
                     if (at == 0) a.work.ml[(size_t)slot * kN + row] = make_float2(m, lsum);
                 } else {
-                    out[out_at(row) + at] = __float2bfloat16_rn(acc[r] * inv);
-                }
-                // (a row that sees NaN itself has it in its sum: nothing to repair)
-                if (lsum * 0.f == 0.f && __any_sync(0xffffffffu, !(acc[r] * 0.f == 0.f))) {
-                    __syncwarp();
-                    const int token = row / g.G;
-                    const float4 o =
-                        paged::repair_row<kCodes>(a, d, token, d.h * g.G + row - token * g.G, m, scale_log2);
-                    if ((lane >> 3) == ww) {  // lane l has features 4 l ..: this warp's 32
-                        if (cut)
-                            *reinterpret_cast<float4*>(part + row * kD + 4 * lane) = o;
-                        else
-                            *reinterpret_cast<uint2*>(out + out_at(row) + 4 * lane) =
-                                make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
-                    }
-                    __syncwarp();
+                    // (a value that it does not see may be NaN where all others see it)
+                    out[out_at(row) + at] = __float2bfloat16_rn(lsum == 0.f ? 0.f : acc[r] * inv);
                 }
             }
             if (cut) {

@@ -16,9 +16,8 @@
 //
 // Roles: warp 0 loads (TMA: Q tiles, and each block's pages, found through
 // the page table, into the rings of K and V tiles), warp 1 issues the products,
-// warp 2 holds the TMEM, warp 3 clears the slots behind the last key of a page
-// (bf16 pages: what lies there may be NaN, and 0 x NaN is not 0), warps 4-11
-// are the two softmax warpgroups and write the outputs.
+// warp 2 holds the TMEM, warp 3 (bf16 pages) cleans V's blocks at the mask's
+// edges, warps 4-11 are the two softmax warpgroups and write the outputs.
 //
 // Pages of codes.  S takes K's codes as they are, with Q as the sum of two e4m3
 // terms: q 2^k = hi + lo, k per row so that the largest element lies in [2^7,
@@ -36,9 +35,9 @@
 // by more than 2^8, which rescales O.
 //
 // Masked scores become -inf before the maximum: a weight of exactly 0.  What
-// a masked V row holds still enters 0 x v: if that is not finite, O is not,
-// and the rows it hit are computed again with plain loads of the keys they
-// see (repair_row): slow, and only for such rows.
+// a masked V row holds still enters 0 x v: warp 3 takes what is not finite out of
+// blocks that some query of the tile does not see all of (clean_block), and
+// the queries that do see it get it back at the end (give_back).
 //
 // Bound by the softmax's chain per block (scores from TMEM, maximum, weights,
 // half a P V, the next S: about 3400 cycles for two halves, of which the
@@ -114,12 +113,12 @@ struct __align__(1024) Smem {
     // (for the loading warp)
     static constexpr int kK = C::kK, kKBytes = C::kKBytes, kVLoads = 2;
     static constexpr uint32_t kQHalf = kHalfBytes;
-    static constexpr bool kClearTail = !kCodes;  // (a code, NaN's too, becomes a finite bf16)
+    static constexpr bool kClean = !kCodes;  // (a code, NaN's too, becomes a finite bf16)
     __device__ uint64_t* q_landed(int s) { return kCodes ? &q_raw[s] : &q_full[s]; }
     __device__ uint64_t* v_landed(int s) { return kCodes ? &st_full[s] : &v_full[s]; }
     __device__ uint64_t* v_taken(int s) { return kCodes ? &st_empty[s] : &v_empty[s]; }
     __device__ uint8_t* v_load(int s) { return kCodes ? st[s] : v[s]; }
-    uint64_t v_tail;             // a ragged block of V has landed, its tail not cleared yet
+    uint64_t v_edge[kVLoads];    // a block of V that some query does not see all of has landed, not cleaned yet
     uint64_t s_full[2];          // S of warpgroup w's item is in TMEM
     uint64_t p_half[2], p_full[2];  // 4 warp arrivals: P of the last / first 64 keys written
     uint64_t pv_half[2];         // an item's first half of P V is in O_w
@@ -196,6 +195,58 @@ __device__ __forceinline__ RowOf row_of(const Desc& d, int row, int wg, int G, i
     return r;
 }
 
+// The softmax warp's rows (one a thread) of the piece in a slot of sm.desc that
+// had values taken out, after their outputs or partials were written: first
+// which features hold such values at all, then their sums over the keys that
+// the row sees.  (All of it worked out again, and few registers: what the main
+// loop keeps for it, or moves out of its way, costs prompts 250 -> 288 us.)
+static __device__ __noinline__ void give_rows_back(const PagedAttend& a, Smem<false>& sm, int desc) {
+    const Desc& d = sm.desc[desc];
+    const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 7) - 1, row = threadIdx.x & 127;
+    const bool pair = d.pair != 0, cut = d.c0 != d.c1;
+    const RowOf r = row_of(d, row, wg, a.g.G, kRows / a.g.G);
+    const paged::Seen seen = paged::seen_by(a.mask, d);
+    paged::Sight mine{0, 0, 0};
+    if (r.valid) mine = paged::sight(a.mask, d.at0 + r.token, d.total);
+    uint32_t hit = 0u;
+    paged::for_edge_keys(a, d, seen, [&](const __nv_bfloat16* v, int) {
+#pragma unroll 8
+        for (int u = 0; u < paged::kEdgeKeys; ++u) {
+            const uint2 w = *reinterpret_cast<const uint2*>(v + u * kD + 4 * lane);
+            hit |= paged::not_finite_bf16(w.x) | paged::not_finite_bf16(w.y);
+        }
+    });
+    uint32_t quads = __ballot_sync(0xffffffffu, hit != 0u);  // of four features
+    if (!pair) quads &= wg ? 0xffff0000u : 0x0000ffffu;       // (a tile of one half: this warpgroup's columns)
+    for (; quads; quads &= quads - 1) {
+        const int quad = __ffs(quads) - 1;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        paged::for_edge_keys(a, d, seen, [&](const __nv_bfloat16* v, int j) {
+#pragma unroll 8
+            for (int u = 0; u < paged::kEdgeKeys; ++u) {
+                const uint2 w = *reinterpret_cast<const uint2*>(v + u * kD + 4 * quad);
+                const uint32_t x = paged::not_finite_bf16(w.x), y = paged::not_finite_bf16(w.y);
+                if ((x | y) && paged::sees(mine, j + u) && !paged::sees(seen.all, j + u)) {
+                    if (x & 0x8000u) sum[0] += __uint_as_float(w.x << 16);
+                    if (x >> 16) sum[1] += __uint_as_float(w.x & 0xffff0000u);
+                    if (y & 0x8000u) sum[2] += __uint_as_float(w.y << 16);
+                    if (y >> 16) sum[3] += __uint_as_float(w.y & 0xffff0000u);
+                }
+            }
+        });
+        if (sum[0] == 0.f && sum[1] == 0.f && sum[2] == 0.f && sum[3] == 0.f) continue;
+        if (cut) {
+            const size_t slot = (size_t)paged::partial_slot(sm.pl, blockIdx.x, d.base) * 2 + (pair ? wg : 0);
+            float4& o = reinterpret_cast<float4*>(a.work.o)[(slot * 32 + quad) * kRows + row];
+            o = make_float4(o.x + sum[0], o.y + sum[1], o.z + sum[2], o.w + sum[3]);
+        } else {
+            __nv_bfloat16* o =
+                static_cast<__nv_bfloat16*>(a.out) + ((size_t)(d.row0 + r.token) * a.g.Hq + r.head) * kD + 4 * quad;
+            for (int c = 0; c < 4; ++c) o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + sum[c]);
+        }
+    }
+}
+
 template <bool kCodes>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -226,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             init(&sm.v_full[i], kCodes ? kConvWarps : 1);
             init(&sm.v_empty[i], 1);
+            init(&sm.v_edge[i], 1);
             init(&sm.st_full[i], 1);
             init(&sm.st_empty[i], kConvWarps);
             init(&sm.q_raw[i], 1);
@@ -237,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             init(&sm.pv_half[i], 1);
             init(&sm.pv_done[i], 1);
         }
-        init(&sm.v_tail, 1);
         init(&sm.o_free, kSoftmaxWarps);
         init(&sm.ebar, kSoftmaxWarps);
         init(&sm.drain, 1);
@@ -369,31 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_wait_bounded(ptx::smem_u32(&sm.drain), 0, &no_abort, kWaitLimitNs);
         }
     } else if (!kCodes && warp == 3) {
-        // ----------------------------------- slots behind the last key --
-        if constexpr (!kCodes) {
-            int vn = 0, tails = 0;
-            bool ok = true;
-            for (int si = 0; ok; ++si) {
-                Desc d;
-                if (!get_desc(si, d)) {
-                    ok = false;
-                    break;
-                }
-                if (d.done) break;
-                const int n = d.b1 - d.b0;
-                if (n <= 0) continue;
-                vn += n;
-                const int key0 = d.key0(n - 1);
-                if (key0 + kKB <= d.total) continue;
-                ok = wwait(&sm.v_tail, tails & 1);
-                ++tails;
-                if (!ok) break;
-                const int s = (vn - 1) & 1;  // the piece's last tile
-                paged::clear_tail(sm.v[s], 2, key0, d.total);
-                arrive1(&sm.v_full[s]);
-            }
-            if (!ok) fail();
-        }
+        // -------------------------- what is hidden in V and not finite --
+        if constexpr (!kCodes)
+            if (!paged::clean_pieces<false>(sm, a.mask, get_desc, wwait)) fail();
     } else if (kCodes && warp < 4) {
         // ----------------- Q in two terms, V's codes -> bf16 tiles --
         if constexpr (kCodes) {
@@ -758,7 +787,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = cut ? paged::partial_slot(sm.pl, blockIdx.x, d.base) : 0;
             const int half = pair ? wg : 0;
             float4* part = reinterpret_cast<float4*>(a.work.o) + (size_t)slot * 2 * 32 * kRows + half * 32 * kRows + row;
-            float zero = 0.f;
             if (busy) {
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
@@ -774,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) {
                         const float x0 = use0 ? f0 * __uint_as_float(o0[i]) : 0.f;
                         acc[i] = use1 ? fmaf(f1, __uint_as_float(o1[i]), x0) : x0;
-                        zero = fmaf(acc[i], 0.f, zero);
+                        if (l == 0.f) acc[i] = 0.f;  // (a value that it does not see may be NaN where all others see it)
                     }
                     if (valid && cut) {
 #pragma unroll
@@ -797,28 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_before();
             if (n > 0) arrive1(&sm.o_free);
             if constexpr (!kCodes) {
-                uint32_t hurt = __ballot_sync(0xffffffffu, valid && !(zero == 0.f) && l * 0.f == 0.f);  // (a NaN sum: the row sees NaN itself)
-                __syncwarp();
-                while (hurt) {
-                    const int src = __ffs(hurt) - 1;
-                    hurt &= hurt - 1;
-                    const int r_token = __shfl_sync(0xffffffffu, token, src);
-                    const int r_head = __shfl_sync(0xffffffffu, head, src);
-                    const float r_m = __shfl_sync(0xffffffffu, m, src);
-                    const float r_inv = __shfl_sync(0xffffffffu, inv, src);
-                    const float4 o = paged::repair_row<false>(a, d, r_token, r_head, r_m, scale_log2);
-                    if (4 * lane >= col0 && 4 * lane < col0 + 32 * chunks) {
-                        if (cut) {
-                            part[lane * kRows + src - lane] = o;
-                        } else {
-                            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) +
-                                                ((size_t)(d.row0 + r_token) * g.Hq + r_head) * kD + 4 * lane;
-                            *reinterpret_cast<uint2*>(to) = make_uint2(ptx::pack_bf16x2(o.x * r_inv, o.y * r_inv),
-                                                                       ptx::pack_bf16x2(o.z * r_inv, o.w * r_inv));
-                        }
-                    }
-                    __syncwarp();
-                }
+                if (d.taken && busy) give_rows_back(a, sm, si % kDescs);
             }
             if (!cut) {
                 arrive1(&sm.d_empty[si % kDescs]);

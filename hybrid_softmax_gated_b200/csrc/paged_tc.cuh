@@ -1,6 +1,6 @@
 // Parts shared by the tensor-core kernels over the paged cache: the pieces of
-// work as their roles see them, the loading warp, and the repair of rows that a
-// hidden value which is not finite has spoilt.
+// work as their roles see them, the loading warp, and what keeps hidden values
+// that are not finite out of the products.
 #pragma once
 
 #include "paged.cuh"
@@ -33,6 +33,7 @@ struct Desc {
     int pair;                // the tile has two halves
     int c0, c1;              // CTAs that share the tile
     long long base;
+    int taken;               // values that are not finite were taken out of the products (clean_block)
     // first key of this CTA's block j
     __device__ int key0(int j) const {
         const int i = b0 + j;
@@ -44,56 +45,114 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// One output row again, by a whole warp, with plain loads: O = sum over the
-// keys it sees of the blocks [b0, b1) of exp2(score - m) v, lane l holding
-// features 4 l .. 4 l + 3.
-template <bool kCodes>
-static __device__ __noinline__ float4 repair_row(const PagedAttend& a, const Desc& d, int token, int head, float m,
-                                                 float scale_log2) {
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16* q =
-        static_cast<const __nv_bfloat16*>(a.q) + (long long)(d.row0 + token) * a.q_stride + head * kD + 4 * lane;
-    float qf[4];
-    for (int c = 0; c < 4; ++c) qf[c] = to_float(q[c]);
-    const Sight see = sight(a.mask, d.at0 + token, d.total);
-    const float base = m == -INFINITY ? 0.f : m;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int bi = d.b0; bi < d.b1; ++bi) {
-        const int key0 = d.key0(bi - d.b0);
-        for (int j = key0; j < key0 + kKB; ++j) {
-            if (!sees(see, j)) continue;
-            const int page = a.seqs.table[(size_t)d.s * a.seqs.max_pages + (j >> a.g.page_log2)];
-            if ((unsigned)page >= (unsigned)a.g.pages) continue;  // (reported by the loader)
-            const size_t row = pool_row(a.g, page, d.h, j), at = row * kD + 4 * lane;
-            float k[4], v[4];
-            for (int c = 0; c < 4; ++c) {
-                if constexpr (kCodes) {
-                    k[c] = to_float(static_cast<const __nv_fp8_e4m3*>(a.pool.k)[at + c]) * a.pool.ks[row];
-                    v[c] = to_float(static_cast<const __nv_fp8_e4m3*>(a.pool.v)[at + c]) * a.pool.vs[row];
-                } else {
-                    k[c] = to_float(static_cast<const __nv_bfloat16*>(a.pool.k)[at + c]);
-                    v[c] = to_float(static_cast<const __nv_bfloat16*>(a.pool.v)[at + c]);
-                }
-            }
-            float s = 0.f;
-            for (int c = 0; c < 4; ++c) s = fmaf(qf[c], k[c], s);
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float p = ptx::ex2(fmaf(s, scale_log2, -base));
-            for (int c = 0; c < 4; ++c) acc[c] = fmaf(p, v[c], acc[c]);
-        }
+// Keys that all of a tile's queries see, and that some of them see (the
+// queries at positions before 0, which see nothing, left out).  Ends, lower
+// ends and sinks all move right with a query's position, and each window
+// starts no later than the previous one ends.
+struct Seen {
+    Sight all, any;
+    // nothing of the block at key0 is hidden from anybody
+    __device__ __forceinline__ bool open(int key0) const {
+        return key0 + kKB <= all.end && (key0 >= all.lo || key0 + kKB <= all.sink);
     }
-    return make_float4(acc[0], acc[1], acc[2], acc[3]);
+};
+__device__ __forceinline__ Seen seen_by(const PagedMask& m, const Desc& d) {
+    const Sight first = sight(m, d.at0 < 0 ? 0 : d.at0, d.total), last = sight(m, d.at0 + d.n - 1, d.total);
+    return Seen{Sight{first.end, last.lo, first.sink}, Sight{last.end, first.lo, last.sink}};
 }
 
-// The slots of the block at key0 behind the sequence's last key, in a tile of
-// `halves` x 128 rows of 128 bytes: zeros (what lies in a page there may be NaN,
-// and 0 x NaN is not 0).  By one warp.
-__device__ __forceinline__ void clear_tail(uint8_t* tile, int halves, int key0, int total) {
-    const int first = total > key0 ? total - key0 : 0;
-    for (int half = 0; half < halves; ++half)
-        for (int at = first * 128 + (threadIdx.x & 31) * 16; at < (int)kHalfBytes; at += 512)
-            *reinterpret_cast<uint4*>(tile + half * kHalfBytes + at) = make_uint4(0u, 0u, 0u, 0u);
+// What a block of V at key0 holds for keys that not all of the tile's queries
+// see, in a tile of 128-byte rows (bf16: two halves of 128 rows): a weight of 0
+// hides a finite value only, 0 x NaN is not 0.  Keys that nobody sees (behind
+// the last one, too) become zeros.  Of the others what is not finite becomes
+// zero: an element of bf16 (returns whether there was one: the queries that see
+// it get it back from give_back), a code (its scale is NaN, and so are the
+// weights of those that see it).  By one warp.
+template <bool kCodes>
+__device__ __forceinline__ bool clean_block(uint8_t* tile, int key0, const Seen& seen) {
+    constexpr int kHalves = kCodes ? 1 : 2, kStep = 16;  // keys whose loads are in flight together
+    constexpr uint32_t kMax = kCodes ? 0x7f7f7f7fu : 0x7f807f80u, kOne = kCodes ? 0x01010101u : 0x00800080u;
+    constexpr uint32_t kTop = kCodes ? 0x80808080u : 0x80008000u, kFull = kCodes ? 0xffu : 0xffffu;
+    constexpr int kShift = kCodes ? 7 : 15;
+    // (a code of ones, an exponent of ones: the sum's carry)
+    auto hits = [&](uint32_t w) { return ((w & kMax) + kOne) & kTop; };
+    const int lane = threadIdx.x & 31;
+    bool found = false;
+    for (int r = 0; r < kKB; r += kStep) {
+        const int key = key0 + r;
+        if (key + kStep <= seen.all.end && (key >= seen.all.lo || key + kStep <= seen.all.sink)) continue;
+        uint8_t* const base = tile + r * 128 + lane * 16;  // of the lane's 16 bytes of key r + lane / 8 + 4 i: 512 i on
+        auto at = [&](int i) { return reinterpret_cast<uint4*>(base + (i >> 2) * kHalfBytes + (i & 3) * 512); };
+        if (key >= seen.any.end || (key >= seen.any.sink && key + kStep <= seen.any.lo)) {
+#pragma unroll
+            for (int i = 0; i < 4 * kHalves; ++i) *at(i) = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        uint4 u[4 * kHalves];
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves; ++i) u[i] = *at(i);
+        uint32_t bad = 0u;
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves; ++i) {
+            if constexpr (kCodes) {
+                bad |= hits(u[i].x) | hits(u[i].y) | hits(u[i].z) | hits(u[i].w);
+            } else {
+                auto mag = [](uint32_t x) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)); };
+                const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(mag(u[i].x), mag(u[i].y)), __hmax2_nan(mag(u[i].z), mag(u[i].w)));
+                bad |= hits(*reinterpret_cast<const uint32_t*>(&m));
+            }
+        }
+        // (rare: so are steps with keys that nobody sees among others)
+        const bool some_none = !(key + kStep <= seen.any.end && (key >= seen.any.lo || key + kStep <= seen.any.sink));
+        if (bad || some_none) {
+#pragma unroll 1
+            for (int i = 0; i < 4 * kHalves; ++i) {
+                const int k = key + (lane >> 3) + 4 * (i & 3);
+                if (!sees(seen.any, k)) {
+                    *at(i) = make_uint4(0u, 0u, 0u, 0u);
+                } else if (!sees(seen.all, k)) {
+                    uint4 x = *at(i);
+                    uint32_t was = 0u;
+                    auto clear = [&](uint32_t& w) {
+                        const uint32_t hit = hits(w);
+                        was |= hit;
+                        w &= ~((hit >> kShift) * kFull);
+                    };
+                    clear(x.x), clear(x.y), clear(x.z), clear(x.w);
+                    if (was) {
+                        *at(i) = x;
+                        found = true;
+                    }
+                }
+            }
+        }
+    }
     ptx::fence_proxy_async_smem();
+    return __any_sync(0xffffffffu, found);
+}
+
+// What clean_block has taken out goes to the outputs of the rows that see it: it
+// is an infinity or NaN, and a weight is positive, so it is added as it is.  Only
+// keys at the mask's edges are looked at, at most as many as a block and the tile
+// have tokens.  Calls use(values, key) for 16 keys at a time of this CTA's
+// blocks, `values` their rows in the pool (16 keys share a page; the end of a page
+// that is seen in part is read as well, the slots are there).  bf16 pages.
+constexpr int kEdgeKeys = 16;
+template <class Use>
+__device__ __forceinline__ void for_edge_keys(const PagedAttend& a, const Desc& d, const Seen& seen, Use use) {
+    for (int bi = d.b0; bi < d.b1; ++bi) {
+        const int key0 = d.key0(bi - d.b0);
+        if (seen.open(key0)) continue;
+        for (int j = key0; j < key0 + kKB; j += kEdgeKeys) {
+            if (j >= seen.any.end || (j >= seen.any.sink && j + kEdgeKeys <= seen.any.lo)) continue;
+            const int page = a.seqs.table[(size_t)d.s * a.seqs.max_pages + (j >> a.g.page_log2)];
+            if ((unsigned)page < (unsigned)a.g.pages)  // (else reported by the loader)
+                use(static_cast<const __nv_bfloat16*>(a.pool.v) + pool_row(a.g, page, d.h, j) * kD, j);
+        }
+    }
+}
+__device__ __forceinline__ uint32_t not_finite_bf16(uint32_t w) {  // bit 15, bit 31
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
 // The first `rows` rows of a Q tile (two swizzled halves of 64 features), in
@@ -159,8 +218,7 @@ struct Places {
     const PagedAttend* a;
     const Desc* d;
     int n, pb_log2, batch_log2, span, absent;  // blocks; pages of a block, blocks of a batch, keys of a page's share
-    int see_lo;
-    Sight last;      // keys that some query sees: [0, last.sink) and [see_lo, last.end)
+    Seen seen;
     int at;          // batch of p0
     int p0, p1, raw; // places of batches at and at + 1; what the table says of at + 2
     bool need;
@@ -170,7 +228,7 @@ struct Places {
     __device__ __forceinline__ void look_up(int batch) {
         const int lane = threadIdx.x & 31, j = (batch << batch_log2) + (lane >> pb_log2);
         const int k0 = d->key0(j) + ((lane & (per_block() - 1)) << a->g.page_log2);
-        need = j < n && k0 < last.end && (k0 + span > see_lo || k0 < last.sink);
+        need = j < n && k0 < seen.any.end && (k0 + span > seen.any.lo || k0 < seen.any.sink);
         raw = need ? a->seqs.table[(size_t)d->s * a->seqs.max_pages + (k0 >> a->g.page_log2)] : 0;
     }
     __device__ __forceinline__ int found() const {
@@ -186,8 +244,7 @@ struct Places {
         batch_log2 = 5 - pb_log2;
         span = page_tokens < kKB ? page_tokens : kKB;
         absent = a->g.pages * a->g.Hk;
-        last = sight(a->mask, d->at0 + d->n - 1, d->total);
-        see_lo = sight(a->mask, d->at0 < 0 ? 0 : d->at0, d->total).lo;
+        seen = seen_by(a->mask, d_);
         at = 0;
         look_up(0);
         const bool n0 = need;
@@ -237,6 +294,32 @@ struct Ring {
     }
 };
 
+// Cleans the blocks that need it, of all pieces in order, in a warp of its own:
+// from the slot's v_edge barrier (the loader's) to its v_full.  get_desc and
+// wwait: the kernel's.  Returns false if a wait ran out.
+template <bool kCodes, class S, class Get, class Wait>
+__device__ __forceinline__ bool clean_pieces(S& sm, const PagedMask& m, Get get_desc, Wait wwait) {
+    Ring<S::kVLoads> vr;
+    uint32_t odd = 0;  // parities of the slots' v_edge
+    for (int si = 0;; ++si) {
+        Desc d;
+        if (!get_desc(si, d)) return false;
+        if (d.done) return true;
+        const Seen seen = seen_by(m, d);
+        for (int j = 0; j < d.b1 - d.b0; ++j, vr.next()) {
+            const int key0 = d.key0(j), s = vr.slot;
+            if (seen.open(key0)) continue;
+            if (!wwait(&sm.v_edge[s], (odd >> s) & 1)) return false;
+            odd ^= 1u << s;
+            // (the softmax warps hold the piece's descriptor until its end, and
+            // look at it after the products with this block)
+            if (clean_block<kCodes>(sm.v_load(s), key0, seen)) sm.desc[si % kDescs].taken = 1;
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_u32(sm.v_landed(s)));
+        }
+    }
+}
+
 template <bool kCodes, class S>
 struct Loader {
     S& sm;
@@ -244,7 +327,8 @@ struct Loader {
     const CUtensorMap &tm_q, &tm_k, &tm_v;
     Ring<S::kK> kr;
     Ring<S::kVLoads> vr;
-    int qn = 0, tails = 0, tail_use = 0;  // (tail_use: the V ring's use that was the last tail)
+    int qn = 0;
+    uint32_t edges = 0, edge_odd = 0;  // V slots that ever held a block to be cleaned; an odd number of them
 
     // Q tiles of the piece
     template <class Wait>
@@ -293,15 +377,11 @@ struct Loader {
         const int lane = threadIdx.x & 31, s = vr.slot, place = pl.of(j), slot0 = pl.slot0(j);
         if (vr.waits() && !wwait(sm.v_taken(s), vr.parity())) return false;
         uint64_t* full = sm.v_landed(s);
-        if (S::kClearTail && j == pl.n - 1 && pl.d->key0(j) + kKB > pl.d->total) {
-            // a warp of its own clears the tail and hands the tile on; one at a
-            // time (the previous one's slot, if not in use again, tells)
-            if (tails && vr.uses - tail_use < S::kVLoads &&
-                !wwait(sm.v_landed(tail_use % S::kVLoads), (tail_use / S::kVLoads) & 1))
-                return false;
-            full = &sm.v_tail;
-            tail_use = vr.uses;
-            ++tails;
+        if (S::kClean && !pl.seen.open(pl.d->key0(j))) {
+            // another warp cleans the block and hands it on
+            full = &sm.v_edge[s];
+            edges |= 1u << s;
+            edge_odd ^= 1u << s;
         }
         const uint32_t bar = ptx::smem_u32(full);
         ptx::mbar_arrive_expect_tx_w(bar, kCodes ? kCodeTile : kTileBytes);
@@ -322,7 +402,9 @@ struct Loader {
             ptx::mbar_wait_bounded(ptx::smem_u32(bar), use & 1, &no_abort, kWaitLimitNs);
         };
         for (int i = kr.uses > S::kK ? kr.uses - S::kK : 0; i < kr.uses; ++i) landed(&sm.k_full[i % S::kK], i / S::kK);
-        if (tails) landed(&sm.v_tail, tails - 1);
+        if constexpr (S::kClean)
+            for (int i = 0; i < S::kVLoads; ++i)
+                if (edges >> i & 1) landed(&sm.v_edge[i], (edge_odd >> i & 1) ^ 1);
         for (int i = vr.uses > S::kVLoads ? vr.uses - S::kVLoads : 0; i < vr.uses; ++i)
             landed(sm.v_landed(i % S::kVLoads), i / S::kVLoads);
         for (int i = qn > 2 ? qn - 2 : 0; i < qn; ++i) landed(sm.q_landed(i & 1), i >> 1);
@@ -364,7 +446,7 @@ __device__ __forceinline__ bool load_pieces(S& sm, const CUtensorMap& tm_q, cons
         const bool pair = pc.n > tl.half;
         const Desc d{0,          cur.s,        cur.h,        pc.q.q0 + pc.i0, pc.n,  pc.q.total - pc.q.n + pc.i0,
                      pc.q.total, pc.blocks.ns, pc.blocks.w0, pc.b0,           pc.b1, pair,
-                     pc.c0,      pc.c1,        cur.base};
+                     pc.c0,      pc.c1,        cur.base,     0};
         if (lane == 0) sm.desc[slot] = d;
         arrive1(&sm.d_full[slot]);
         const int n = pc.b1 - pc.b0;

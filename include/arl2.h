@@ -524,9 +524,9 @@ arl2_status arl2_paged_read(arl2_paged_handle* h, const arl2_paged_pool* pool, i
  * with v: to bf16, or, for at most 16 query rows of a key head and E4M3, to 12
  * bits; with E4M3 they take q to within 2^-17 of its row's largest element.
  * Pages none of whose keys a query of the chunk sees are not looked up (a
- * rolling cache may have given them away).  A key that is not finite and that
- * only some queries of the same 128 see costs those queries' rows a slow second
- * computation.  One launch. */
+ * rolling cache may have given them away).  A value that is not finite reaches
+ * the queries that see it, as what it is; if not all queries of a tile see it,
+ * the keys at the mask's edges are looked at twice more.  One launch. */
 arl2_status arl2_paged_attend(arl2_paged_handle* h, const arl2_paged_pool* pool, const arl2_paged_batch* batch,
                               int block, int window, int sinks, const void* q, long long q_stride, void* out,
                               cudaStream_t stream);

@@ -179,3 +179,104 @@ def test_a_device_without_an_index_is_the_current_one():
     cache.write(k, k, batch)
     cache.attend(k, batch)
     assert torch.equal(cache.read(table, offsets, 5)[0], k) and cache.device_status() == 0
+
+
+# ---- values that are not finite -------------------------------------------------
+
+def loaded(case, impl="auto", max_ctas=0):
+    cache = PagedCache(case.hq, case.hk, case.d, case.pages, case.page, dtype=case.dtype, cache_format=case.store,
+                       impl=impl, max_ctas=max_ctas)
+    raw(cache.k_pages)[0].copy_(raw(case.kp))
+    raw(cache.v_pages)[0].copy_(raw(case.vp))
+    if case.store == "e4m3":
+        cache.k_scales[0].copy_(case.ks)
+        cache.v_scales[0].copy_(case.vs)
+    batch = PagedBatch(case.q_offsets.cuda(), case.kv_lens.cuda(), case.table.cuda(), max_new=max(n for n, _ in case.lens))
+    return cache, batch
+
+
+def spoil(cache, case, s, j, head, feature, x):
+    """Key j's value of sequence s: not finite (codes: the whole row)."""
+    at = int(case.table[s, j // case.page]), j % case.page
+    if case.store == "e4m3":
+        cache.v_scales[0, at[0], head, at[1]] = float("nan")
+    else:
+        cache.v_pages[0, at[0], head, at[1], feature] = x
+
+
+@pytest.mark.parametrize("store", ["native", "e4m3"])
+@pytest.mark.parametrize("hq,hk", [(2, 2), (6, 2), (2, 1)])
+@pytest.mark.parametrize("new,total,block,window,sinks", [
+    (3, 700, 1, 0, 0), (8, 3000, 1, 500, 20), (5, 900, 3, 40, 7), (300, 1500, 1, 0, 0), (300, 1500, 1, 400, 300),
+    (280, 1400, 100, 3, 1), (150, 2000, 1000, 1, 0), (600, 600, 1, 0, 0),
+])
+@pytest.mark.parametrize("max_ctas", [0, 5])
+def test_a_value_reaches_the_queries_that_see_it_and_no_other(store, hq, hk, new, total, block, window, sinks, max_ctas):
+    """A value that is not finite: the queries that do not see it, other
+    heads and other sequences are bit for bit as before; those that see it have
+    it, in its feature."""
+    case = ref.Case([(new, total), (min(new, 90), 200)], hq, hk, store=store, seed=new + hq, page=64)
+    cache, batch = loaded(case, max_ctas=max_ctas)
+    q, g = case.q.cuda(), hq // hk
+    kw = dict(block=block, window=window, sinks=sinks)
+    clean = cache.attend(q, batch, **kw)
+    sight = np.stack([ref.bounds(total - new + i, total, block, window, sinks) for i in range(new)])
+    some = [j for j in range(total) if sight[:, j].any() and not sight[:, j].all()]
+    near = some[len(some) // 3] if some else total - 1
+    spots = [(near, 5, float("inf")), (near, 70, float("nan")), (total - 1, 5, float("inf")),
+             (max(0, total - 2), 64, float("-inf")), (total - new // 2 - 1, 64, float("inf")), (0, 127, float("nan"))]
+    gone = [(int(case.table[0, j // 64]), j % 64) for j in range(total) if not sight[:, j].any()]
+    for p, sl in gone:  # keys that nobody sees
+        (cache.v_scales if store == "e4m3" else cache.v_pages)[0, p, :, sl] = float("nan")
+        if store == "e4m3":
+            raw(cache.v_pages)[0, p, :, sl] = 0x7f
+    assert torch.equal(cache.attend(q, batch, **kw), clean)
+    for j, f, x in spots:
+        spoil(cache, case, 0, j, 0, f, x)
+    got = cache.attend(q, batch, **kw)
+    assert cache.device_status() == 0
+    want = clean.clone()
+    held = {(j, f): x for j, f, x in spots}  # (the same element twice: the last one)
+    for i in range(new):
+        for (j, f), x in held.items():
+            if sight[i, j]:
+                want[i, :g, slice(None) if store == "e4m3" else f] += x
+    assert torch.equal(got.isnan(), want.isnan())
+    where = ~want.isnan()
+    # (an element that is not finite leaves its row's other features alone)
+    assert torch.equal(got[where], want[where])
+
+
+@pytest.mark.parametrize("store", ["native", "e4m3"])
+@pytest.mark.parametrize("new", [8, 1000])
+def test_a_value_that_is_not_finite_costs_no_second_computation(store, new):
+    """One such value, seen by all, by some or by few queries of a chunk on a
+    long history: right, and not slower by more than the keys at the mask's edge."""
+    total = 30000
+    case = ref.Case([(new, total), (5, 400)], 2, 2, store=store, seed=3, page=256)
+    cache, batch = loaded(case)
+    q = case.q.cuda()
+
+    def timed():
+        torch.cuda.synchronize()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        cache.attend(q, batch)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b)
+
+    clean = cache.attend(q, batch)
+    usual = min(timed() for _ in range(5))
+    for hurt in (100, total - new // 2, total - 2):
+        raw(cache.v_pages)[0].copy_(raw(case.vp))
+        if store == "e4m3":
+            cache.v_scales[0].copy_(case.vs)
+        spoil(cache, case, 0, hurt, 0, 5, float("nan"))
+        got = cache.attend(q, batch)
+        first = max(0, hurt - (total - new))  # of the queries that see it
+        assert torch.isnan(got[first:new, 0, 5]).all()
+        assert torch.equal(got[:first], clean[:first]) and torch.equal(got[new:], clean[new:])
+        assert torch.equal(got[:, 1], clean[:, 1])
+        assert min(timed() for _ in range(3)) < 5 * usual + 0.3  # milliseconds
+        assert cache.device_status() == 0
