@@ -770,6 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = meet();  // (all have read: the next piece may write)
                 if (!ok) break;
             }
+            if constexpr (kCodes)  // (a padded row's query may be NaN: its scores are NaN, not -inf, where they are hidden)
+                if (d.at0 + token < 0) l = 0.f;
             for (int w = 0; ok && w < 2; ++w) {
                 if (!has[w]) continue;
                 if (!pair || w == wg) ok = wwait(&sm.pv_done[w], (pv_par >> w) & 1);

@@ -280,3 +280,29 @@ def test_a_value_that_is_not_finite_costs_no_second_computation(store, new):
         assert torch.equal(got[:, 1], clean[:, 1])
         assert min(timed() for _ in range(3)) < 5 * usual + 0.3  # milliseconds
         assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("store", ["native", "e4m3"])
+@pytest.mark.parametrize("lens", [[(40, 25), (3, 60)], [(300, 200), (5, 90)], [(6, 3), (2, 1)], [(200, 130), (150, 700)],
+                                  [(8, 0), (1, 5)]])
+@pytest.mark.parametrize("max_ctas", [0, 1])
+def test_padding_on_the_left_may_hold_anything(store, lens, max_ctas):
+    """Rows at negative positions: zeros, whatever their queries and the
+    others' values are."""
+    case = ref.Case(lens, 4, 2, store=store, seed=7, page=16)
+    cache, batch = loaded(case, max_ctas=max_ctas)
+    clean = cache.attend(case.q.cuda(), batch)
+    q = case.q.cuda()
+    pad = torch.zeros(case.tokens, dtype=torch.bool)
+    for s, (n, t) in enumerate(lens):
+        pad[int(case.q_offsets[s]):int(case.q_offsets[s]) + max(0, n - t)] = True
+    for i, at in enumerate(pad.nonzero().flatten().tolist()):
+        q[at] = [float("nan"), float("inf"), float("-inf"), 3e38][i % 4]
+    got = cache.attend(q, batch)
+    assert cache.device_status() == 0
+    assert torch.equal(got, clean) and (got[pad.cuda()] == 0).all()
+    s, t = next((s, t) for s, (_, t) in enumerate(lens) if t)
+    spoil(cache, case, s, t // 2, 0, 9, float("nan"))
+    got = cache.attend(q, batch)
+    assert (got[pad.cuda()] == 0).all()
+    assert torch.equal(got[:, 2:], clean[:, 2:])
