@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t* to = pt + r * 128 + (spot ^ ((r & 7) << 4));
                     if constexpr (kCodes) {
                         float w = p * vs;
-                        if (masked && p == 0.f) w = 0.f;  // (a hidden value's scale may be anything)
+                        if (masked && x[r] == -INFINITY) w = 0.f;  // (a hidden value's scale may be anything)
 #pragma unroll
                         for (int t = 0; t < 3; ++t) {
                             const uint32_t code = e4m3_of(w);

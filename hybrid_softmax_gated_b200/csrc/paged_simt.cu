@@ -6,8 +6,8 @@
 // one key head) against blocks of 64 keys, with the online softmax: a block's
 // scores S = Q K^T in 16 x 16 threads of RM x 4 each, the rows' running
 // maximum and sum, then O += P V with O in registers.  A masked key's weight
-// is an exact zero and its value is not multiplied, so it has no effect
-// whatever it holds.  The CTAs split all tiles' blocks evenly and merge a cut
+// is marked (-1) and its value is not multiplied, so it has no effect
+// whatever it holds; a weight that rounds to 0 is multiplied (0 x NaN is NaN).  The CTAs split all tiles' blocks evenly and merge a cut
 // tile's partials (paged.cuh).  Bound by the fp32 pipes: per 4 features of
 // the products a thread loads RM + 4 vectors from shared memory for 16 RM
 // multiply-adds (12 to 16 TFLOP/s on long chunks); short calls by one block's
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
                 float sum = 0.f;
                 for (int j = part; j < kKB; j += kPerRow) {
                     const float x = sm.p[r][j];
-                    const float e = x == -INFINITY ? 0.f : exp2f(x - base);
-                    sm.p[r][j] = e;
+                    const float e = exp2f(x - base);  // (x = -inf: 0)
+                    sm.p[r][j] = x == -INFINITY ? -1.f : e;
                     sum += e;
                 }
 #pragma unroll
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
 #pragma unroll
                 for (int i = 0; i < RM; ++i) {
                     const float p = sm.p[ty * RM + i][j];
-                    if (p != 0.f) {
+                    if (!(p < 0.f)) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             o[i][c].x = fmaf(p, vv[c].x, o[i][c].x);

@@ -641,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 qs[r] = ptx::add2(qs[r], p);
                                 float2 w = ptx::mul2(p, v2);
                                 if (masked) {  // (a hidden value's scale may be anything)
-                                    w.x = p.x == 0.f ? 0.f : w.x;
-                                    w.y = p.y == 0.f ? 0.f : w.y;
+                                    w.x = x.x == -INFINITY ? 0.f : w.x;
+                                    w.y = x.y == -INFINITY ? 0.f : w.y;
                                 }
                                 pk[r >> 1][2 * i + (r & 1)] = ptx::pack_bf16x2(w.x, w.y);
                             }

@@ -306,3 +306,34 @@ def test_padding_on_the_left_may_hold_anything(store, lens, max_ctas):
     got = cache.attend(q, batch)
     assert (got[pad.cuda()] == 0).all()
     assert torch.equal(got[:, 2:], clean[:, 2:])
+
+
+@pytest.mark.parametrize("dtype,store,impl", [(BF16, "native", "auto"), (BF16, "e4m3", "auto"), (FP32, "native", "auto"),
+                                              (FP32, "e4m3", "auto"), (BF16, "e4m3", "simt"), (BF16, "native", "simt")])
+@pytest.mark.parametrize("new", [1, 6, 100])
+def test_a_value_counts_however_small_its_weight(dtype, store, impl, new):
+    """A value that is not finite and has a weight that rounds to 0 reaches the
+    queries that see it all the same: 0 x infinity is no number."""
+    total = 300
+    case = ref.Case([(new, total)], 2, 2, dtype=dtype, store=store, seed=13, page=32)
+    case.q = torch.ones_like(case.q)
+    case.kp, case.ks = case.kp.float() * 0 + 1, None  # scores of 0 ...
+    for j in (total - 2, total - new, 40):
+        case.kp[int(case.table[0, j // 32]), :, j % 32] = -100.0  # ... and of -1143
+    if store == "e4m3":
+        case.kp, case.ks = ref.quantise(case.kp)
+    else:
+        case.kp = case.kp.to(dtype)
+    cache, batch = loaded(case, impl)
+    q = case.q.cuda()
+    clean = cache.attend(q, batch)
+    assert torch.isfinite(clean).all()
+    for j in (total - 2, total - new, 40):
+        raw(cache.v_pages)[0].copy_(raw(case.vp))
+        if store == "e4m3":
+            cache.v_scales[0].copy_(case.vs)
+        spoil(cache, case, 0, j, 0, 77, float("inf"))
+        got = cache.attend(q, batch)
+        first = max(0, j - (total - new))
+        assert not torch.isfinite(got[first:, 0, 77]).any(), j
+        assert torch.equal(got[:first], clean[:first]) and torch.equal(got[:, 1], clean[:, 1])
