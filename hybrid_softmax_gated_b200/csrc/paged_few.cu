@@ -24,7 +24,10 @@
 // scores against it.  A row's maximum over the block takes a reduction in each
 // warp and one exchange between the four warps of the warpgroup.  It is a
 // lazy base c: weights are 2^(score - c), and c moves only when a weight would
-// pass the terms' range, which rescales O.  The two warpgroups take alternate
+// pass the terms' range, which rescales O.  With codes O has a base of its own,
+// o: it differs from c only where all values that weigh in a row have scales
+// below 2^-93, whose weights alone would not fit fp32 at the terms' range (down
+// to 2^-126 they are 2^133).  The two warpgroups take alternate
 // blocks, with their own bases and accumulators; the epilogue combines them.
 // 48 streams of up to 12000 keys (32 heads on 8): 237 us, 6.5 TB/s, the rate of
 // a copy; 64 streams with a window of 8192 keys over e4m3 pages: 183 us, 5.8 TB/s.
@@ -59,7 +62,8 @@ constexpr uint32_t kColS = 0, kColO = 128;  // four S buffers of 32 columns; O_0
 constexpr float kTopBits = 7.f;           // codes: the largest weight is 2^7 when c is set ...
 constexpr float kLazyCodes = 1.75f;       // ... and may grow to 2^8.75 (e4m3 ends at 448 = 2^8.8)
 constexpr float kLazyBf16 = 8.f;
-constexpr float kLeastScale = -100.f;     // sums count from 2^-100 of the largest weight at least
+constexpr float kLeastScale = -100.f;     // c: weights up to 2^(100 + kLazyCodes), whose sums fit fp32
+constexpr float kLeastCode = -126.f - kTopBits;  // o: of the least scale of a row
 
 template <bool kCodes>
 struct __align__(1024) Smem {
@@ -82,8 +86,10 @@ struct __align__(1024) Smem {
     __device__ float* ks(int blk) { return reinterpret_cast<float*>(scratch) + blk % kScaleSlots * 2 * kKB; }
     __device__ float* vs(int blk) { return ks(blk) + kKB; }
     float row_scale[4][kN];
-    float top[2][2][kWgWarps][kN];            // [warpgroup][item & 1][warp][row]: block maxima
-    float red_l[kSoftmaxWarps][kN], red_c[2][kN];
+    float top[2][2][kWgWarps][kN];            // [warpgroup][item & 1][warp][row]: block maxima for c
+    float o_top[kCodes ? 2 : 1][2][kWgWarps][kN];  // and for o, where they differ in some row:
+    __align__(4) uint8_t o_apart[2][2][kWgWarps];
+    float red_l[kSoftmaxWarps][kN], red_c[2][kN], red_o[2][kN];
     uint64_t d_full[kDescs], d_empty[kDescs];
     uint64_t q_raw[2], q_full[2], q_empty[2];
     uint64_t k_full[kK], k_empty[kK];
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // lane r looks after row r: what it sees, its base
             paged::Sight see{1 << 30, 0, 0};
             if (lane < rows) see = paged::sight(a.mask, d.at0 + lane / g.G, d.total);
-            float c = -INFINITY;
+            float c = -INFINITY, ob = -INFINITY;
             float l[NR], row_mul[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -392,12 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = d.key0(j);
                 const bool open = key0 + kKB <= see.end && (key0 >= see.lo || key0 + kKB <= see.sink);
                 const bool masked = __any_sync(0xffffffffu, !open);
-                float ks = 1.f, vs = 1.f, grow = 0.f;
+                float ks = 1.f, vs = 1.f, grow = 0.f, o_grow = 0.f;
+                bool small = false;  // (warp-uniform) some scale is below what c can follow
                 if constexpr (kCodes) {
                     ks = sm.ks(blk + j)[at];
                     vs = sm.vs(blk + j)[at];
                     // a weight's size against its score's: the terms' range, and the sum's
-                    grow = fmaxf(__log2f(vs) - kTopBits, kLeastScale);
+                    o_grow = fmaxf(__log2f(vs) - kTopBits, kLeastCode);
+                    grow = fmaxf(o_grow, kLeastScale);
+                    small = __any_sync(0xffffffffu, vs > 0.f && o_grow < kLeastScale);
                 }
                 ptx::tmem_wait_ld();
                 ptx::reg_fence16(y);
@@ -430,19 +439,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == r) top = m;
                 }
                 float(&tops)[kWgWarps][kN] = sm.top[wg][(j >> 1) & 1];
+                float(&o_tops)[kWgWarps][kN] = sm.o_top[kCodes ? wg : 0][(j >> 1) & 1];
                 if (lane < NR) tops[ww][lane] = top;
+                if constexpr (kCodes) {
+                    if (lane == 0) sm.o_apart[wg][(j >> 1) & 1][ww] = small;
+                    float o_top = top;
+                    if (__builtin_expect(small, 0)) {
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            const float m = warp_max(x[r] + o_grow);
+                            if (lane == r) o_top = m;
+                        }
+                    }
+                    if (lane < NR) o_tops[ww][lane] = o_top;
+                }
                 arrive1(&sm.wbar[wg]);
                 ok = wwait(&sm.wbar[wg], (w_uses++) & 1);
                 if (!ok) break;
-                float fac = 1.f;
-                bool need = false;
-                if (lane < NR) {
-                    const float z = ptx::max3(tops[0][lane], tops[1][lane], fmaxf(tops[2][lane], tops[3][lane]));
-                    need = z > c + (kCodes ? kLazyCodes : kLazyBf16);
-                    if (need) {
-                        fac = ptx::ex2(c - z);
-                        c = z;
-                    }
+                constexpr float kLazy = kCodes ? kLazyCodes : kLazyBf16;
+                const int mine = lane & (NR - 1);
+                auto highest = [&](const float(&t)[kWgWarps][kN]) {
+                    return ptx::max3(t[0][mine], t[1][mine], fmaxf(t[2][mine], t[3][mine]));
+                };
+                const float z = highest(tops);
+                bool need = z > c + kLazy;
+                const float fac = need ? ptx::ex2(c - z) : 1.f;  // of the sums
+                c = need ? z : c;
+                float o_fac = fac;                                // of O
+                if constexpr (kCodes) {
+                    float zo = z;
+                    if (*reinterpret_cast<const uint32_t*>(sm.o_apart[wg][(j >> 1) & 1])) zo = highest(o_tops);
+                    const bool o_need = zo > ob + kLazy;
+                    o_fac = o_need ? ptx::ex2(ob - zo) : 1.f;
+                    ob = o_need ? zo : ob;
+                    need = need || o_need;
                 }
                 const bool rescale = __any_sync(0xffffffffu, need);
                 const float base = c == -INFINITY ? 0.f : c;  // nothing seen yet: weights 2^-inf
@@ -462,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ptx::reg_fence16(o);
 #pragma unroll
                             for (int r = 0; r < NR; ++r)
-                                o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, fac, r));
+                                o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, o_fac, r));
                             ptx::tmem_st16(obuf + 16u * t, o);
                         }
                         ptx::tmem_wait_st();
@@ -473,6 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // weights -> P^T, K-major rows of 128 keys
                 uint8_t* pt = sm.p[wg];
                 const uint32_t spot = kCodes ? (uint32_t)at : (uint32_t)((at >> 6) * (kN * 128) + (at & 63) * 2);
+                // (always: a branch, which the compiler makes two loops of, costs 0.7 us of
+                // instruction fetches in a short call)
+                const float up = c != ob ? ptx::ex2(c - ob) : 1.f;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     const float p = ptx::ex2(x[r] - __shfl_sync(0xffffffffu, base, r));
@@ -480,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t* to = pt + r * 128 + (spot ^ ((r & 7) << 4));
                     if constexpr (kCodes) {
                         float w = p * vs;
+                        w *= __shfl_sync(0xffffffffu, up, r);
                         if (masked && x[r] == -INFINITY) w = 0.f;  // (a hidden value's scale may be anything)
 #pragma unroll
                         for (int t = 0; t < 3; ++t) {
@@ -507,7 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
                 if (lane == 0) sm.red_l[warp - 4][r] = l[r];
             }
-            if (ww == 0 && lane < NR) sm.red_c[wg][lane] = c;
+            if (ww == 0 && lane < NR) {
+                sm.red_c[wg][lane] = c;
+                sm.red_o[wg][lane] = kCodes ? ob : c;
+            }
             // the last P V of each warpgroup (its own is waited for here, the
             // other's by the meeting)
             if (wg < n) {
@@ -549,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int r = 0; r < NR / 2; ++r) {
                     const float c0 = sm.red_c[0][r0 + r], c1 = sm.red_c[1][r0 + r];
                     const float m = fmaxf(c0, c1);
-                    const float f0 = c0 == -INFINITY ? 1.f : ptx::ex2(c0 - m), f1 = c1 == -INFINITY ? 1.f : ptx::ex2(c1 - m);
+                    const float o0 = sm.red_o[0][r0 + r], o1 = sm.red_o[1][r0 + r];
+                    const float f0 = c0 == -INFINITY ? 1.f : ptx::ex2(o0 - m), f1 = c1 == -INFINITY ? 1.f : ptx::ex2(o1 - m);
                     acc[r] = (has0 ? f0 * pick(0, r) : 0.f) + (has1 ? f1 * pick(1, r) : 0.f);
                 }
             }

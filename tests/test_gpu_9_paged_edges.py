@@ -337,3 +337,38 @@ def test_a_value_counts_however_small_its_weight(dtype, store, impl, new):
         first = max(0, j - (total - new))
         assert not torch.isfinite(got[first:, 0, 77]).any(), j
         assert torch.equal(got[:first], clean[:first]) and torch.equal(got[:, 1], clean[:, 1])
+
+
+@pytest.mark.parametrize("gain", [1.0, 1e-27, 1e-30, 1e-34, 1e30])
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 40)], [(4, 700), (2, 90)]])
+@pytest.mark.parametrize("max_ctas", [0, 3])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_weights_of_few_rows_over_codes(gain, lens, max_ctas, mixed):
+    """Few query rows over codes: weights to 12 bits, however small or large all
+    of a row's values are; mixed: every seventh value row is of zeros, every
+    fifth a thousand times smaller.
+
+    Off by: the output's rounding; a weight's three terms (2^-12 of the weight, and
+    2^-25 of the row's largest weight times value scale, counted against a value of
+    448 scales: 2^-16 of the largest contribution); q in two terms, 2^-17 of its
+    row's largest element in each of d products, which moves a score by delta and the
+    weights by 2 delta; fp32 sums as in the other tests."""
+    case = ref.Case(lens, 4, 1, store="e4m3", seed=31, page=32)
+    g = torch.Generator().manual_seed(37)
+    x = gain * torch.randn(case.vp.shape, generator=g)
+    if mixed:
+        x[:, :, ::7] = 0.0
+        x[:, :, ::5] *= 1e-3
+    case.vp, case.vs = ref.quantise(x)
+    cache, batch = loaded(case, max_ctas=max_ctas)
+    out = cache.attend(case.q.cuda(), batch)
+    assert cache.device_status() == 0
+    got = out.double().cpu().numpy()
+    want, absolute, slack = case.expect()
+    v = np.abs(case.values("v").numpy()).max()
+    n, q, k = max(t for _, t in lens), case.q.double().abs(), case.values("k").abs().max().item()
+    delta = (2.0 ** -17 * q.amax(-1, keepdim=True) * k * 128 * 128 ** -0.5).numpy()
+    tol = 2.0 ** -8 * np.abs(want) + absolute * (2 * slack + 2 * delta + (16 + n / 16) * 2.0 ** -24 + 2.0 ** -12) \
+        + 2.0 ** -16 * v
+    bad = ~(np.abs(got - want) <= 1.01 * tol)
+    assert not bad.any(), (np.abs(got - want)[bad][:4], tol[bad][:4], want[bad][:4])
