@@ -36,6 +36,7 @@ constexpr int kMaxGroup = 64;
 constexpr int kMaxCtasPerSm = 8;
 constexpr int kFewRows = 16;  // query rows of a key head up to which the transposed kernel runs
 constexpr long long kMaxKeys = 1ll << 30;
+constexpr int kMaxTokens = 1 << 30;  // (with what a kernel's blocks take on top it still fits an int)
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -76,7 +77,7 @@ arl2_status check_pool(const arl2_paged_handle* h, const arl2_paged_pool* p) {
 }
 
 arl2_status check_tables(const arl2_paged_handle* h, int seqs, int tokens, int max_pages) {
-    if (seqs < 0 || seqs > arl2::kPagedMaxSeqs || tokens < 0 || max_pages < 0 ||
+    if (seqs < 0 || seqs > arl2::kPagedMaxSeqs || tokens < 0 || tokens > kMaxTokens || max_pages < 0 ||
         ((long long)max_pages << h->g.page_log2) > kMaxKeys)
         return ARL2_ERR_SHAPE;
     return ARL2_OK;

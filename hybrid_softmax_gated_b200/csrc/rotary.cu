@@ -26,6 +26,7 @@ namespace {
 constexpr int kMaxPairs = 128;
 constexpr int kThreads = 256;
 constexpr int kMaxTokensPerBlock = 32;
+constexpr int kMaxTokens = 1 << 30;  // (with a block's tokens on top it still fits an int)
 constexpr int kInFlight = 4;  // heads of an item, all their loads on their way together
 
 // The plan as the kernel gets it (1.2 KB of launch parameters).
@@ -283,7 +284,7 @@ arl2_status arl2_rotary_apply(const arl2_rotary* r, arl2_dtype dtype, int tokens
                               long long q_out_stride, int k_heads, const void* k, long long k_stride,
                               void* k_out, long long k_out_stride, int inverse, cudaStream_t stream) {
     if (!r || (dtype != ARL2_BF16 && dtype != ARL2_FP32)) return ARL2_ERR_INVALID_ARG;
-    if (tokens < 0 || q_heads < 0 || k_heads < 0 || q_heads > 1024 || k_heads > 1024) return ARL2_ERR_SHAPE;
+    if (tokens < 0 || tokens > arl2::kMaxTokens || q_heads < 0 || k_heads < 0 || q_heads > 1024 || k_heads > 1024) return ARL2_ERR_SHAPE;
     if (tokens == 0 || q_heads + k_heads == 0) return ARL2_OK;
     if (!positions || (q_heads && (!q || !q_out)) || (k_heads && (!k || !k_out))) return ARL2_ERR_INVALID_ARG;
     const int d = r->plan.d;

@@ -392,7 +392,7 @@ arl2_status arl2_rotary_create(const arl2_rotary_config* cfg, arl2_rotary** out)
  * dense) by positions (device int32 [tokens][axes], any sign) into q_out and
  * k_out, in one launch.  An output may be its own input (in place) but not
  * overlap any tensor otherwise.  q_heads or k_heads may be 0 (pointers
- * unused then); tokens may be 0 (nothing to do).  The angle is formed as an
+ * unused then); tokens may be 0 (nothing to do), and 2^30 at most.  The angle is formed as an
  * exact product in 2^-64 turns and reduced before it is rounded, so far
  * positions lose nothing.  Errors: INVALID_ARG, SHAPE, ALIGN (a pointer not
  * aligned to its elements), CUDA. */
@@ -482,7 +482,7 @@ typedef struct {
 
 typedef struct {
     int seqs;              /* 0..1024                                         */
-    int tokens;            /* rows of the token tensors, >= 0                 */
+    int tokens;            /* rows of the token tensors: 0..2^30              */
     int max_pages;         /* columns of page_table; max_pages * page_tokens
                               <= 2^30                                         */
     int max_new;           /* the largest number of new tokens of a sequence,

@@ -2,10 +2,13 @@
 documentation allows and that are easily got wrong: tables out of order, other
 streams and devices, values that are not finite, the smallest and largest
 numbers."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
+import hybrid_softmax_gated_b200 as arl2
 import paged_reference as ref
 from hybrid_softmax_gated_b200 import PagedBatch, PagedCache, RotaryAxes
 
@@ -372,3 +375,20 @@ def test_weights_of_few_rows_over_codes(gain, lens, max_ctas, mixed):
         + 2.0 ** -16 * v
     bad = ~(np.abs(got - want) <= 1.01 * tol)
     assert not bad.any(), (np.abs(got - want)[bad][:4], tol[bad][:4], want[bad][:4])
+
+
+# ---- sizes -----------------------------------------------------------------------
+
+def test_more_tokens_than_an_int_can_count_on_are_refused():
+    """Nothing is launched: the addresses are never used."""
+    cache, batch, q, k, v, positions = step_case()
+    lib, fake, before = arl2._lib, 0x1000, cache.kernel_launches()
+    p = ctypes.byref(cache._pools[0])
+    for tokens in (2 ** 30 + 1, 2 ** 31 - 100, 2 ** 31 - 1):
+        b = ctypes.byref(arl2.Arl2PagedBatch(2, tokens, 10, 1, fake, fake, fake))
+        assert lib.arl2_paged_write(cache.handle, p, b, fake, 0, fake, 0, None) == -2
+        assert lib.arl2_paged_read(cache.handle, p, 2, tokens, 10, fake, None, fake, fake, fake, None) == -2
+        assert lib.arl2_paged_attend(cache.handle, p, b, 1, 0, 0, fake, 0, fake * 2, None) == -2
+        assert lib.arl2_paged_forward(cache.handle, p, b, None, None, 1, 0, 0, fake, 0, fake, 0, fake, 0, None,
+                                      fake * 2, None) == -2
+    assert cache.kernel_launches() == before

@@ -48,3 +48,14 @@ def test_a_pool_is_on_one_device(e4m3):
     else:
         with pytest.raises(ValueError, match="none"):
             arl2._check_pool(pool(False, vs={}), SHAPE, store, False)
+
+
+def test_rotary_takes_at_most_2_30_tokens():
+    plan, fake = arl2.RotaryAxes(2, [2]), 0x1000  # never dereferenced
+
+    def call(tokens):
+        return arl2._lib.arl2_rotary_apply(plan.handle, 0, tokens, fake + 2, 1, fake, 0, fake, 0, 0, None, 0, None, 0, 0, None)
+
+    assert call(2 ** 30) == -3  # (the misaligned positions come next)
+    for tokens in (2 ** 30 + 1, 2 ** 31 - 32, 2 ** 31 - 1):
+        assert call(tokens) == -2
