@@ -609,6 +609,15 @@ def _like(t, stream):
     return _empty(t, t.shape, t.dtype, stream)
 
 
+def _mask(block, window, sinks):
+    """The mask's sizes as C integers: positions stay below 2^30, so what is
+    larger than an int means the same as the largest one (ctypes would take its
+    low 32 bits)."""
+    if (block | window | sinks) >> 31:  # (a negative one, too: refused by the call)
+        block, window, sinks = (max(-1, min(x, 2 ** 31 - 1)) for x in (block, window, sinks))
+    return block, window, sinks
+
+
 class RotaryAxes:
     """Rotary positions with up to four axes (arl2_rotary_* in the C ABI).
 
@@ -701,7 +710,7 @@ class PagedBatch:
         _table(kv_lens, "kv_lens", (seqs,), self.device)
         _table(page_table, "page_table", (seqs, None), self.device)
         self.tensors = (q_offsets, kv_lens, page_table)
-        self.seqs, self.max_new, self.max_pages = seqs, int(max_new), int(page_table.shape[1])
+        self.seqs, self.max_new, self.max_pages = seqs, min(int(max_new), 2 ** 31 - 1), int(page_table.shape[1])
         self._c = {}
 
     def struct(self, tokens: int):
@@ -846,8 +855,8 @@ class PagedCache:
         as they were."""
         self._rows(q, "q", 0)
         out = self._out(out, q, stream)
-        _check(_lib.arl2_paged_attend(self.handle, self._pool(layer), self._batch(batch, q.shape[0]), block, window,
-                                      sinks, q.data_ptr(), _token_stride(q), out.data_ptr(), _stream(stream)),
+        _check(_lib.arl2_paged_attend(self.handle, self._pool(layer), self._batch(batch, q.shape[0]),
+                                      *_mask(block, window, sinks), q.data_ptr(), _token_stride(q), out.data_ptr(), _stream(stream)),
                "arl2_paged_attend")
         return out
 
@@ -867,8 +876,8 @@ class PagedCache:
         out = self._out(out, q, stream)
         _check(_lib.arl2_paged_forward(self.handle, self._pool(layer), self._batch(batch, tokens),
                                        None if rotary is None else rotary.handle,
-                                       None if rotary is None else positions.data_ptr(), block, window, sinks,
-                                       q.data_ptr(), _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
+                                       None if rotary is None else positions.data_ptr(),
+                                       *_mask(block, window, sinks), q.data_ptr(), _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
                                        _token_stride(v), None if turned is None else turned.data_ptr(),
                                        out.data_ptr(), _stream(stream)), "arl2_paged_forward")
         return out

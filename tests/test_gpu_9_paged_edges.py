@@ -392,3 +392,15 @@ def test_more_tokens_than_an_int_can_count_on_are_refused():
         assert lib.arl2_paged_forward(cache.handle, p, b, None, None, 1, 0, 0, fake, 0, fake, 0, fake, 0, None,
                                       fake * 2, None) == -2
     assert cache.kernel_launches() == before
+
+
+def test_a_window_longer_than_an_int_is_no_window():
+    cache, batch, q, k, v, positions = step_case()
+    want = cache.attend(q, batch)
+    for big in (2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
+        assert torch.equal(cache.attend(q, batch, window=big, sinks=big), want)
+        assert torch.equal(cache.forward(q, k, v, batch, window=big), cache.forward(q, k, v, batch))
+        want = cache.attend(q, batch)
+    for kw in (dict(block=-2 ** 32 + 1), dict(window=-2 ** 32 + 5), dict(sinks=-2 ** 63)):
+        with pytest.raises(arl2.Arl2Error):
+            cache.attend(q, batch, **kw)

@@ -59,3 +59,13 @@ def test_rotary_takes_at_most_2_30_tokens():
     assert call(2 ** 30) == -3  # (the misaligned positions come next)
     for tokens in (2 ** 30 + 1, 2 ** 31 - 32, 2 ** 31 - 1):
         assert call(tokens) == -2
+
+
+def test_sizes_of_the_mask_keep_their_meaning():
+    top = 2 ** 31 - 1
+    assert arl2._mask(1, 0, 0) == (1, 0, 0) and arl2._mask(1560, 21, 3) == (1560, 21, 3)
+    for big in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1):
+        assert arl2._mask(1, big, 0) == (1, top, 0)
+        assert arl2._mask(big, 7, big) == (top, 7, top)
+    for low in (-1, -2 ** 32 + 5, -2 ** 63):
+        assert arl2._mask(1, low, 0) == (1, -1, 0)
