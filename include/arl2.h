@@ -523,6 +523,8 @@ arl2_status arl2_paged_read(arl2_paged_handle* h, const arl2_paged_pool* pool, i
  * the softmax weights (times the value's scale, in E4M3) before the product
  * with v: to bf16, or, for at most 16 query rows of a key head and E4M3, to 12
  * bits; with E4M3 they take q to within 2^-17 of its row's largest element.
+ * q, k and v may be 0 or of magnitudes from 2^-100 to 2^100, scores (q.k times
+ * the scale) up to 2^29; beyond, scores, weights or sums may leave fp32's range.
  * Pages none of whose keys a query of the chunk sees are not looked up (a
  * rolling cache may have given them away).  A value that is not finite reaches
  * the queries that see it, as what it is; if not all queries of a tile see it,

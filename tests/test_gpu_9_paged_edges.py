@@ -404,3 +404,42 @@ def test_a_window_longer_than_an_int_is_no_window():
     for kw in (dict(block=-2 ** 32 + 1), dict(window=-2 ** 32 + 5), dict(sinks=-2 ** 63)):
         with pytest.raises(arl2.Arl2Error):
             cache.attend(q, batch, **kw)
+
+
+@pytest.mark.parametrize("dtype,store,impl", [(BF16, "native", "auto"), (BF16, "e4m3", "auto"), (FP32, "native", "auto"),
+                                              (BF16, "e4m3", "simt")])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("keys,queries,values", [
+    (1.0, 5e6, 1.0), (1e29, 5e-23, 1e29), (1e-29, 1e29, 1e-29), (1e-29, 1e-29, 1e29), (1e29, 1e-29, 1e-29),
+])
+def test_magnitudes_over_the_documented_range(dtype, store, impl, new, keys, queries, values):
+    """Keys, queries and values from 2^-100 to 2^100, scores up to 2^29: where one
+    key's score stands out by more than the scores' rounding, its value; scores
+    near 0: within the usual bounds, relative to the values."""
+    case = ref.Case([(new, 300), (new, 90)], 4, 2, dtype=dtype, store=store, seed=41, page=32)
+    g = torch.Generator().manual_seed(43)
+    case.q = (queries * torch.randn(case.q.shape, generator=g)).to(dtype)
+    for name, gain in (("k", keys), ("v", values)):
+        x = gain * torch.randn(case.kp.shape, generator=g)
+        pages, scales = ref.quantise(x) if store == "e4m3" else (x.to(dtype), None)
+        setattr(case, name + "p", pages), setattr(case, name + "s", scales)
+    cache, batch = loaded(case, impl)
+    got = cache.attend(case.q.cuda(), batch).double().cpu().numpy()
+    assert cache.device_status() == 0 and np.isfinite(got).all()
+    want, absolute, slack = case.expect()
+    sharp = 0
+    for s, (n, t) in enumerate(case.lens):
+        at, k, v = int(case.q_offsets[s]), case.sequence("k", s), case.sequence("v", s)
+        for i in range(n):
+            for h in range(4):
+                score = k[:t - n + i + 1, h // 2] @ case.q[at + i, h].double().numpy() * 128 ** -0.5
+                # (q of codes is off by 2^-17 of its row's largest in each of 128 products, fp32 sums by `slack`)
+                off = slack[at + i, h, 0] + 2.0 ** -17 * 128 ** 0.5 * case.q[at + i, h].double().abs().max().item() * np.abs(k).max()
+                order = np.argsort(score)
+                if off < 0.0099:  # (weights move by a factor of e^(2 off) <= 1 + 2.02 off)
+                    bound = case.tolerance(want, absolute, slack, impl) - 1.01e-30 + 2.02 * 2 * off * absolute
+                    assert (np.abs(got - want) <= bound)[at + i, h].all()
+                elif score[order[-1]] - score[order[-2]] > 2 * off + 40:
+                    sharp += 1
+                    assert (np.abs(got[at + i, h] - v[order[-1], h // 2]) <= 2.0 ** -7 * np.abs(v[order[-1], h // 2])).all()
+    assert sharp or off < 0.0099
