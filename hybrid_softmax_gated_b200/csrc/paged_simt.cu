@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttend a, flo
                 for (int j = part; j < kKB; j += kPerRow) {
                     const float x = sm.p[r][j];
                     const float e = exp2f(x - base);  // (x = -inf: 0)
-                    sm.p[r][j] = x == -INFINITY ? -1.f : e;
+                    // (a visible score may be -inf, too)
+                    sm.p[r][j] = x == -INFINITY && !paged::sees(sm.see[r], key0 + j) ? -1.f : e;
                     sum += e;
                 }
 #pragma unroll

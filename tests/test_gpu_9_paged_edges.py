@@ -340,6 +340,10 @@ def test_a_value_counts_however_small_its_weight(dtype, store, impl, new):
         first = max(0, j - (total - new))
         assert not torch.isfinite(got[first:, 0, 77]).any(), j
         assert torch.equal(got[:first], clean[:first]) and torch.equal(got[:, 1], clean[:, 1])
+        if store == "native":  # the key is infinite as well: a weight of 0 exactly
+            cache.k_pages[0, int(case.table[0, j // 32]), 0, j % 32, 3] = float("-inf")
+            assert not torch.isfinite(cache.attend(q, batch)[first:, 0, 77]).any(), j
+            raw(cache.k_pages)[0].copy_(raw(case.kp))
 
 
 @pytest.mark.parametrize("gain", [1.0, 1e-27, 1e-30, 1e-34, 1e30])
