@@ -611,6 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < NR / 2; ++r) {
                 const int row = r0 + r;
                 if (row >= rows) continue;
+                // (a row before the sequence sees nothing, whatever the values that all others see hold)
+                if (d.at0 + row / g.G < 0) acc[r] = 0.f;
                 const float c0 = sm.red_c[0][row], c1 = sm.red_c[1][row];
                 const float m = fmaxf(c0, c1);
                 const float f0 = c0 == -INFINITY ? 1.f : ptx::ex2(c0 - m), f1 = c1 == -INFINITY ? 1.f : ptx::ex2(c1 - m);
@@ -626,8 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[row * kD + at] = acc[r];
                     if (at == 0) a.work.ml[(size_t)slot * kN + row] = make_float2(m, lsum);
                 } else {
-                    // (a value that it does not see may be NaN where all others see it)
-                    out[out_at(row) + at] = __float2bfloat16_rn(lsum == 0.f ? 0.f : acc[r] * inv);
+                    out[out_at(row) + at] = __float2bfloat16_rn(acc[r] * inv);
                 }
             }
             if (cut) {
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         if (r0 + r < rows)
-                            out[out_at(r0 + r) + at] = __float2bfloat16_rn(ll[r] == 0.f ? 0.f : oo[r] / ll[r]);
+                            out[out_at(r0 + r) + at] = __float2bfloat16_rn(oo[r] * (ll[r] == 0.f ? 0.f : 1.f / ll[r]));
                 }
             } else {
                 // (red_l and red_c have been read: the next piece may write them)

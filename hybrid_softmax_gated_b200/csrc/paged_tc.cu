@@ -770,8 +770,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = meet();  // (all have read: the next piece may write)
                 if (!ok) break;
             }
-            if constexpr (kCodes)  // (a padded row's query may be NaN: its scores are NaN, not -inf, where they are hidden)
-                if (d.at0 + token < 0) l = 0.f;
+            // A row before the sequence sees nothing, whatever its query (NaN makes
+            // hidden scores of codes NaN) and the values that all others see hold.
+            const bool before = d.at0 + token < 0;
+            if (before) l = 0.f;
             for (int w = 0; ok && w < 2; ++w) {
                 if (!has[w]) continue;
                 if (!pair || w == wg) ok = wwait(&sm.pv_done[w], (pv_par >> w) & 1);
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) {
                         const float x0 = use0 ? f0 * __uint_as_float(o0[i]) : 0.f;
                         acc[i] = use1 ? fmaf(f1, __uint_as_float(o1[i]), x0) : x0;
-                        if (l == 0.f) acc[i] = 0.f;  // (a value that it does not see may be NaN where all others see it)
+                        if (before) acc[i] = 0.f;
                     }
                     if (valid && cut) {
 #pragma unroll

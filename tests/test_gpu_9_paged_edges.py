@@ -381,6 +381,28 @@ def test_weights_of_few_rows_over_codes(gain, lens, max_ctas, mixed):
     assert not bad.any(), (np.abs(got - want)[bad][:4], tol[bad][:4], want[bad][:4])
 
 
+@pytest.mark.parametrize("dtype,impl", [(BF16, "auto"), (FP32, "auto"), (BF16, "simt")])
+@pytest.mark.parametrize("new,max_ctas", [(1, 0), (1, 2), (40, 0), (40, 3), (5, 1)])
+def test_weights_of_nothing_but_minus_infinity(dtype, impl, new, max_ctas):
+    """Queries all of whose scores are -infinity: every weight is 0, so a finite
+    value gives 0 and one that is not finite no number."""
+    case = ref.Case([(new, 600), (3, 700)], 2, 2, dtype=dtype, seed=47, page=32)
+    case.q = torch.ones_like(case.q)
+    cache, batch = loaded(case, impl, max_ctas)
+    q = case.q.cuda()
+    other = cache.attend(q, batch)[new:]
+    for j in range(600):
+        cache.k_pages[0, int(case.table[0, j // 32]), :, j % 32, 8] = float("-inf")
+    assert (cache.attend(q, batch)[:new] == 0).all()
+    spoil(cache, case, 0, 11, 0, 77, float("inf"))
+    spoil(cache, case, 0, 599, 1, 12, float("-inf"))
+    got = cache.attend(q, batch)
+    assert torch.equal(got[new:], other) and cache.device_status() == 0
+    assert not torch.isfinite(got[:new, 0, 77]).any() and not torch.isfinite(got[new - 1, 1, 12])
+    got[:new, 0, 77], got[new - 1, 1, 12] = 0, 0
+    assert (got[:new] == 0).all()
+
+
 # ---- sizes -----------------------------------------------------------------------
 
 def test_more_tokens_than_an_int_can_count_on_are_refused():
