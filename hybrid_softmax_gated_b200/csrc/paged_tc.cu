@@ -541,9 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::reg_fence(y);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            // (after the key's scale, which may be anything where the key is hidden)
+                            // (after the key's scale, which may be anything where the key is hidden;
+                            // a value's scale that is not finite makes the score NaN, and with it the row)
                             if constexpr (kCodes)
-                                y[i] = __float_as_uint(__uint_as_float(y[i]) * kscale[32 * c + i]);
+                                y[i] = __float_as_uint(fmaf(vscale[32 * c + i], 0.f, __uint_as_float(y[i]) * kscale[32 * c + i]));
                             y[i] = (seen >> i) & 1u ? y[i] : 0xff800000u;
                         }
                         ptx::tmem_st32(sbuf + (uint32_t)c * 32, y);
@@ -641,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 qs[r] = ptx::add2(qs[r], p);
                                 float2 w = ptx::mul2(p, v2);
                                 if (masked) {  // (a hidden value's scale may be anything)
-                                    w.x = x.x == -INFINITY ? 0.f : w.x;
-                                    w.y = x.y == -INFINITY ? 0.f : w.y;
+                                    w.x = p.x == 0.f ? 0.f : w.x;
+                                    w.y = p.y == 0.f ? 0.f : w.y;
                                 }
                                 pk[r >> 1][2 * i + (r & 1)] = ptx::pack_bf16x2(w.x, w.y);
                             }
@@ -804,9 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float acc[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float x0 = use0 ? f0 * __uint_as_float(o0[i]) : 0.f;
-                        acc[i] = use1 ? fmaf(f1, __uint_as_float(o1[i]), x0) : x0;
-                        if (before) acc[i] = 0.f;
+                        const float x0 = use0 && !before ? f0 * __uint_as_float(o0[i]) : 0.f;
+                        acc[i] = use1 && !before ? fmaf(f1, __uint_as_float(o1[i]), x0) : x0;
                     }
                     if (valid && cut) {
 #pragma unroll
