@@ -625,7 +625,9 @@ class RotaryAxes:
     is left of head_dim passes through).  pairs: "adjacent" (2p, 2p + 1) or
     "halves" (p, p + R/2).  freqs: "per_axis" (each axis runs through all
     frequencies) or "shared" (one run over all axes' pairs).  A plan holds no
-    device memory and may be used on any device, stream and thread.
+    device memory and may be used on any device, stream and thread.  Nothing is
+    recorded for autograd: a backward pass calls apply with inverse=True on the
+    gradients.
     """
 
     def __init__(self, head_dim: int, axis_dims, *, base: float = 10000.0, pairs: str = "adjacent",
@@ -749,7 +751,10 @@ class PagedCache:
     Calls take a stream (a torch stream or a raw handle; default: the current
     one).  What they return may be used on that stream and, once the caller has
     made it wait, on the current one; what they are given has to outlive the
-    kernels (record_stream, for a tensor of another stream).
+    kernels (record_stream, for a tensor of another stream).  The calls of one
+    cache share its workspace: on different streams, or in graphs replayed side
+    by side, they must not overlap (two caches may share a pool).  Nothing is
+    recorded for autograd.
     """
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, pages: int, page_tokens: int, *, layers: int = 1,

@@ -29,8 +29,9 @@
 // below 2^-93, whose weights alone would not fit fp32 at the terms' range (down
 // to 2^-126 they are 2^133).  The two warpgroups take alternate
 // blocks, with their own bases and accumulators; the epilogue combines them.
-// 48 streams of up to 12000 keys (32 heads on 8): 237 us, 6.5 TB/s, the rate of
-// a copy; 64 streams with a window of 8192 keys over e4m3 pages: 183 us, 5.8 TB/s.
+// 48 streams of up to 12000 keys (32 heads on 8): 236 to 242 us, 6.5 TB/s, the
+// rate of a copy; 64 streams with a window of 8192 keys over e4m3 pages: 182 to
+// 194 us (170 in the first launches), 5.5 to 5.8 TB/s.
 //
 // Schedule, loads and what keeps hidden values that are not finite out of the
 // products: paged_tc.cuh.
@@ -54,7 +55,9 @@ using paged::kWgWarps;
 constexpr int kThreads = 384;
 constexpr int kN = 16;                    // columns of a term (query rows)
 // For the schedule, in blocks: what a tile costs on top of its blocks, up to
-// what it is not cut, and how much a CTA has at least.
+// what it is not cut, and how much a CTA has at least.  (With no cost for a tile
+// and short ones cut, four streams of 300 keys take 16.7 us, not 12.4; with the
+// cost but short ones cut, 16 streams of 1000 keys 26.0, not 16.8.)
 constexpr int kTileCost = 4, kWhole = 16, kMinUnits = 8;
 static_assert(kMinUnits > kTileCost, "one border at most in what a tile costs for itself");
 constexpr uint32_t kTmemCols = 256;

@@ -9,8 +9,9 @@
 // generic form, a warp per row.  A warp takes a few rows of one token, all
 // their loads in flight together; it finds the token's sequence by a 32-way
 // search of the offsets (one load for up to 32 sequences, two for 1024).  A
-// history of 3 x 9360 tokens of 12 heads read back from codes: 33 us, 5.6 TB/s;
-// four frames of 1560 tokens quantised: 10 us, 3.6 TB/s, most of it instructions.
+// history of 3 x 9360 tokens of 12 heads read back from codes: 31.5 us, 5.9 TB/s;
+// four frames of 1560 tokens quantised: 10.2 us, 3.4 TB/s, most of it the chain from
+// a token's offsets to its page and the conversion's instructions.
 #include "paged.cuh"
 #include "ptx.cuh"
 

@@ -348,8 +348,9 @@ cudaError_t launch_rows(const PagedAttend& a, int max_new, int max_ctas, cudaStr
     // four times the rows
     const long long tiles = ((long long)a.seqs.tokens * a.g.G + 63) / 64 * a.g.Hk;
     const long long keys = (long long)a.seqs.max_pages << a.g.page_log2;
-    // (also when 64-row tiles would leave most SMs without work: 34 tokens of 8
-    // heads on 43 keys 21 -> 16 us; 160 of 24 on 98 keys would take 33, not 27)
+    // (also when 64-row tiles would give work to half of a B200's 148 SMs at most:
+    // 34 tokens of 8 heads on 43 keys 21 -> 16 us; 160 of 24 on 98 keys, above that
+    // border, would take 33, not 27)
     if (a.g.G <= 16 && ((long long)max_new * a.g.G <= 16 || tiles * ((keys + kKB - 1) / kKB) <= 74))
         return launch<T, C, 1>(a, max_ctas, st);
     return launch<T, C, 4>(a, max_ctas, st);

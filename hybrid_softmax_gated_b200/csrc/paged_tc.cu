@@ -41,11 +41,14 @@
 //
 // Bound by the softmax's chain per block (scores from TMEM, maximum, weights,
 // half a P V, the next S: about 3400 cycles for two halves, of which the
-// products take 2048), with codes by the shared memory that the products'
-// operands, V's conversion and the scales share (about 4800 cycles).  One 480p
-// frame over 24 frames (12 heads): 425 us, 845 TFLOP/s, at 1.45 GHz under the
-// power cap; five chunks of prompts (32 heads on 8): 272 us, 900 TFLOP/s; two
-// streams' frames over e4m3 pages: 356 us, 680 TFLOP/s.
+// products take 2048).  With codes it is about 6200 cycles, tile starts and ends
+// included, in which no unit is busy much more than half the time (issue slots 47
+// %, tensor pipe 35 %, SFU 33 %; shared memory 1350 wavefronts of loads and
+// stores and about 2050 of operands and copies): the chain of V's conversion in
+// two warps, P V and the next S.  One 480p frame over 24 frames (12 heads): 415 to
+// 455 us (355 to 400 in the first launches), 790 to 865 TFLOP/s, at 1.45 GHz
+// under the power cap; five chunks of prompts (32 heads on 8): 272 to 300 us, 815
+// to 900 TFLOP/s; two streams' frames over e4m3 pages: 360 to 370 us, 655 to 675.
 #include "paged_tc.cuh"
 
 #include <cmath>
@@ -76,7 +79,9 @@ constexpr int kRegsLaunch = 168, kRegsLow = 96, kRegsHigh = 200;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
 // For the schedule, in quarters of a block of two halves: the cost of a block,
 // of a tile on top of its blocks, up to what a tile is not cut, and how much a
-// CTA has at least.
+// CTA has at least.  (With no cost for a tile prompts take 314 us, not 281, a
+// frame over 24 frames 424, not 437; with the same cost for a half and a quarter
+// of a half as for two halves, two streams' frames over codes 392, not 363.)
 constexpr int kPairCost = 4, kSingleCost = 3, kSmallCost = 2, kTileCost = 6, kWhole = 16, kMinUnits = 8;
 static_assert(kMinUnits > kTileCost, "one border at most in what a tile costs for itself");
 

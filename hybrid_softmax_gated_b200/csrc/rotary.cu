@@ -204,9 +204,10 @@ cudaError_t launch_as(const Plan& p, const Side& q, const Side& k, const int* po
                       cudaStream_t st) {
     using F = Form<T, kHalves, kWide>;
     const int per_head = p.rot / 2 / F::NP + (p.d - p.rot) / F::kTail;
-    // Heads of an item: as many as are in flight, fewer when there are few
-    // tokens (a token's heads then spread over the block's threads); tokens of
-    // a block: what its threads have one item each for
+    // Heads of an item: as many as are in flight, fewer when the items would not
+    // be two blocks of threads on each of a B200's 148 SMs (a token's heads then
+    // spread over the block's threads); tokens of a block: what its threads
+    // have one item each for
     int group = kInFlight, groups;
     while (true) {
         groups = (q.heads + group - 1) / group + (k.heads + group - 1) / group;
